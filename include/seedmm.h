@@ -66,7 +66,8 @@ enum {
                                SEEDMM_NOALLOC_SCRATCH_BYTES                           */
 };
 
-enum { SEEDMM_F32 = 0, SEEDMM_BF16 = 1 };
+enum { SEEDMM_F32 = 0, SEEDMM_BF16 = 1, SEEDMM_I8 = 2 /* dense operators only */ };
+enum { SEEDMM_SOFTMAX = 0, SEEDMM_SIGMOID = 1 };   /* scores of seedmm_route */
 
 /* One seed-coded matrix, or E stacked matrices of one shape (streams concatenated). */
 typedef struct seedmm_mat {
@@ -393,6 +394,114 @@ int seedmm_cache_moe(seedmm_cache *cache, const int32_t *topk_ids_host,
  * call, summed), out[2] hits, out[3] misses (= records copied), out[4] bytes copied
  * host-to-device. */
 int seedmm_cache_stats(const seedmm_cache *cache, uint64_t out[5]);
+
+/*
+ * Dense operators around the routed layer.  A pack keeps everything but its routed experts
+ * in affine 4 bits (Qwen3.8-Flash-Next-NanoSeedLM-P4 card, "Files", and K2-Horizon card,
+ * "This upload": NAME.weight, NAME.scales, NAME.biases in groups of 32 or 64), normalises
+ * the residual stream before each layer and chooses the experts with a router.
+ *
+ * seedmm_q4_gemv -- Y[n] = W X[n] for N activation rows, with W[m][k] = s q + b:
+ *     y[n][m] = x_scale[n] * sum_g ( s[m][g] sum_{k in g} q[m][k] x[n][k]
+ *                                    + b[m][g] sum_{k in g} x[n][k] )
+ *   weight: uint32[M][K/8], code q of column k in word k/8, bits 4*(k%8);
+ *   scales, biases: [M][K/group] of s_dtype (SEEDMM_F32 or SEEDMM_BF16); group 32, 64 or
+ *   128; columns g*group .. g*group + group - 1 form group g;
+ *   x: [N][ldx] of x_dtype (SEEDMM_F32, SEEDMM_BF16 or SEEDMM_I8);  x_scale: fp32[N] with
+ *   SEEDMM_I8 (the value of a code c of row n is c * x_scale[n]), NULL otherwise;
+ *   y: [N][ldy] of y_dtype (SEEDMM_F32 or SEEDMM_BF16), overwritten; columns M .. ldy - 1
+ *   are left as they were.
+ *   Weights are not rounded to the activations' type: the codes enter the matrix
+ *   instructions as integers, products are exact, sums are fp32 (int32 inside a group for
+ *   SEEDMM_I8), and y is rounded once.  The sums run in a fixed order that depends on the
+ *   sizes and types only: the same call gives the same bits.  A row of x with an infinity or NaN gives a row of y
+ *   without finite meaning and leaves the other rows alone.
+ * Errors: SEEDMM_EINVAL (null pointer, M, K or N < 0, M or K above 2^30, another group,
+ * K % group != 0, ldx < K, ldy < M, bad dtype, x_scale missing or given without
+ * SEEDMM_I8), SEEDMM_EALIGN (weight or x not 16-byte aligned, ldx not a multiple of 16
+ * bytes where N > 1, another pointer not aligned to its type), SEEDMM_EHIP.  M = 0 or
+ * N = 0 is an empty success; K = 0 writes zeros.
+ */
+int seedmm_q4_gemv(const uint32_t *weight, const void *scales, const void *biases, int s_dtype,
+                   int group, const void *x, int x_dtype, int ldx, const float *x_scale, void *y,
+                   int y_dtype, int ldy, int M, int K, int N, void *hip_stream);
+
+/*
+ * seedmm_add_norm -- the residual's addition and the root-mean-square norm before a layer
+ * (the stream that seedmm_moe's fp32 output is added to):
+ *     r = x + delta;   out = r / sqrt(mean_h r^2 + eps) * weight
+ *   x: [N][ldx] fp32 or bf16;  delta: [N][ldd] fp32 or bf16, or NULL (r = x);
+ *   weight: [H] fp32 or bf16, or NULL (ones);
+ *   residual: [N][ldr] of x's type receiving r, or NULL; it may be x itself (same ld).
+ *   out: [N][ldo] of out_dtype.  SEEDMM_F32, SEEDMM_BF16: the value, rounded once.
+ *   SEEDMM_I8: codes round(value / scale[n]) in [-127, 127] with scale[n] = max_h |value| /
+ *   127 (at least 2^-126); a row that holds an infinity or NaN gets scale NaN and codes 0.
+ *   scale: fp32[N] with SEEDMM_I8, NULL otherwise.
+ *   r is not rounded before the norm (only where it is stored as bf16); the sum of squares
+ *   is fp32, so a row whose sum of squares passes 3.4e38 has no meaning.  Rows of any ld
+ *   and alignment are taken; rows that start on 16 bytes are faster.  Elements past H are
+ *   left as they were.
+ * Errors: SEEDMM_EINVAL (null pointer, N or H < 0, ld < H, bad dtype, eps negative or not
+ * finite, scale missing or given without SEEDMM_I8), SEEDMM_EALIGN (a pointer not aligned
+ * to its type), SEEDMM_EHIP.  N = 0 or H = 0 is an empty success.
+ */
+int seedmm_add_norm(const void *x, int x_dtype, int64_t ldx, const void *delta, int delta_dtype,
+                    int64_t ldd, const void *weight, int w_dtype, float eps, void *residual,
+                    int64_t ldr, void *out, int out_dtype, int64_t ldo, float *scale, int N, int H,
+                    void *hip_stream);
+
+/*
+ * seedmm_route -- the routing that seedmm_moe takes (barnson.org post, "Why
+ * K2-Horizon-MoVA": sigmoid routers whose bias only selects experts; softmax over the
+ * chosen logits is this library's reading for the others):
+ *   SEEDMM_SOFTMAX: the top_k largest logits of a token; weights = softmax over those.
+ *   SEEDMM_SIGMOID: the top_k largest sigmoid(logit) + bias (bias fp32[E] or NULL; compared
+ *   in 64 bits); weights = sigmoid(logit) over their sum, without the bias.
+ *   logits: [T][ldl] fp32 or bf16;  ids: int32[T][top_k], w: fp32[T][top_k], in falling
+ *   order of score; equal scores go to the lower expert first.
+ *   A logit of -inf or NaN (and a bias of -inf or NaN) masks its expert.  Where fewer than
+ *   top_k experts are left the slots that remain name masked experts, lowest first, with
+ *   weight 0, so the ids of a token are always distinct and in [0, E).
+ * Errors: SEEDMM_EINVAL (null pointer, T < 0, E outside [1, 4096], top_k outside
+ * [1, min(E, 64)], T*top_k >= 2^31, ldl < E, bad dtype or score, a bias with
+ * SEEDMM_SOFTMAX), SEEDMM_EALIGN (a pointer not aligned to its type), SEEDMM_EHIP.
+ */
+int seedmm_route(const void *logits, int l_dtype, int64_t ldl, const float *bias, int score, int T,
+                 int E, int top_k, int32_t *ids, float *w, void *hip_stream);
+
+/*
+ * seedmm_moe_block -- one routed layer with its norm and its router on the residual
+ * stream (the routed layer of the K2-Horizon card, "This upload"):
+ *     r += delta;  x = bf16(r / sqrt(mean r^2 + eps) * norm_weight);
+ *     ids, w = route(router x);  y = seedmm_moe(ids, w, x)
+ * by the calls seedmm_add_norm, seedmm_q4_gemv, seedmm_route and seedmm_moe_ex, with their
+ * results.  y is the next layer's delta.
+ *   block: host struct; device pointers inside.  The router is an [E][H] matrix in affine
+ *   4 bits; P = 3 or 4, or 0 with p4mask (mixed packs).
+ *   r: [T][H] fp32 or bf16, updated in place if delta is not NULL;  delta: [T][H] fp32 or
+ *   bf16, or NULL; it may not overlap r or y;  y: fp32[T][H];  ids: int32[T][top_k] and
+ *   w: fp32[T][top_k] receive the routing (each may be NULL);
+ *   workspace: device scratch of seedmm_moe_block_workspace_bytes(block, T) bytes; overlapping
+ *   calls use different ones.  side: as for seedmm_moe_ex.
+ * Errors: those of the four calls, before anything runs; r, delta, y, norm_weight and the
+ * router's arrays 16-byte aligned.
+ */
+typedef struct seedmm_block {
+    const void *norm_weight;         /* [H] or NULL                                   */
+    const uint32_t *router_weight;   /* [E][H/8]                                      */
+    const void *router_scales;       /* [E][H/group]                                  */
+    const void *router_biases;
+    const float *router_bias;        /* selection bias fp32[E] or NULL (SIGMOID only) */
+    const uint32_t *p4mask;          /* mixed packs, else NULL                        */
+    seedmm_mat gate, up, down;
+    float eps;
+    int norm_dtype, router_dtype, group, score, top_k, E, H, I, P;
+} seedmm_block;
+
+size_t seedmm_moe_block_workspace_bytes(const seedmm_block *block, int T);
+int seedmm_moe_block(const seedmm_block *block, void *r, int r_dtype, const void *delta,
+                     int delta_dtype, float *y, int32_t *ids, float *w, int T, void *workspace,
+                     size_t workspace_bytes, void *hip_stream, const seedmm_side *side);
 
 /* Static description of a status code (the C engine's error convention: a plain C99
  * interface, NanoSeedLM README "How it works"). */

@@ -13,7 +13,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SO = os.path.join(HERE, "libseedmm.so")
 SOURCES = [os.path.join(CSRC, "seedmm.hip"), os.path.join(CSRC, "search.hip"),
-           os.path.join(CSRC, "expert_cache.hip")]
+           os.path.join(CSRC, "expert_cache.hip"), os.path.join(CSRC, "dense.hip")]
 HEADERS = [os.path.join(CSRC, "seed_decode.hpp"), os.path.join(CSRC, "moe_layer.hpp"),
            os.path.join(ROOT, "include", "seedmm.h")]
 

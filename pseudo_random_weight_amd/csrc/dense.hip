@@ -1,0 +1,585 @@
+// dense.hip -- gfx950 kernels of the dense operators around a seed-coded routed layer, and
+// their C ABI: the product with affine 4-bit weights (seedmm_q4_gemv), the residual's
+// addition with the root-mean-square norm (seedmm_add_norm), the router's choice
+// (seedmm_route), and the layer that calls them with the routed experts (seedmm_moe_block).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/seedmm.h"
+#include "moe_layer.hpp"
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ float bf16_to_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+__device__ __forceinline__ uint16_t f32_to_bf16(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+
+// ----------------------------------------------------------------------------------
+// seedmm_q4_gemv.  y[n][m] = sx[n] sum_g ( s[m][g] D[m][g][n] + b[m][g] X[g][n] ) with
+// D = sum of q x over the group's columns and X = sum of x.
+//
+// Both sums are exact products: a code q is an integer of 4 bits, so it enters the matrix
+// instruction without rounding, and the scale multiplies the group's fp32 sum afterwards
+// (a weight s q + b is never rounded to the activation's type).
+//   bf16 x: 16 + q is the bf16 with bits 0x4180 | q << 3, one shift and one and-or for two
+//     codes; the group's accumulator starts at -16 X, which takes the 16 away again (the
+//     offset is at most twice a code, so the cancellation costs one bit of the fp32 sum).
+//   fp32 x: split into three bf16 of 8 bits each (truncated, so the split is exact), three
+//     rows of the same instruction.
+//   int8 x: the integer instruction; D is exact.
+// ----------------------------------------------------------------------------------
+struct Q4Args {
+    const uint32_t* w;   // [M][K/8], code k of a row in word k/8, bits 4 (k%8)
+    const void* s;       // [M][K/group]
+    const void* b;
+    const void* x;       // [N][ldx]
+    const float* xs;     // int8 x: [N]
+    void* y;             // [N][ldy]
+    int M, K, N, ldx, ldy;
+    int y_bf16;
+};
+
+template <bool SF32>
+__device__ __forceinline__ float load_scale(const void* p, int64_t i) {
+    if constexpr (SF32) return ((const float*)p)[i];
+    else return bf16_to_f32(((const uint16_t*)p)[i]);
+}
+
+// One wave's 16 bytes a lane (32 codes of row l % 16, columns 32 (l / 16) ..) become, after
+// a 4 x 4 transposition over the four lane quarters, word j = codes 32 j + 8 q .. + 7 of the
+// 128 columns: each word is then a lane's operand of one 32-column instruction.
+__device__ __forceinline__ void transpose_quarters(uint32_t (&w)[4]) {
+    auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+    auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+    auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    w[0] = c[0]; w[1] = c[1]; w[2] = d[0]; w[3] = d[1];
+}
+
+// 8 codes -> bf16 16 + q in the order 0 4 1 5 2 6 3 7
+__device__ __forceinline__ bf16x8 codes_bf16(uint32_t w) {
+    u32x4 v;
+    v[0] = ((w << 3) & 0x00780078u) | 0x41804180u;
+    v[1] = ((w >> 1) & 0x00780078u) | 0x41804180u;
+    v[2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
+    v[3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
+    return __builtin_bit_cast(bf16x8, v);
+}
+
+// 8 codes -> bytes in the order 0 2 4 6 1 3 5 7
+__device__ __forceinline__ long codes_i8(uint32_t w) {
+    u32x2 v;
+    v[0] = w & 0x0F0F0F0Fu;
+    v[1] = (w >> 4) & 0x0F0F0F0Fu;
+    return __builtin_bit_cast(long, v);
+}
+
+// 16 weight rows a workgroup, its four waves take 128-column steps in turn; the activation
+// rows of a slab of columns are staged in LDS in the operands' order.
+template <int XT, bool SF32, int GROUP>
+__global__ __launch_bounds__(256) void k_q4(const Q4Args a) {
+    constexpr int TOK = XT == SEEDMM_F32 ? 5 : 16;   // tokens a pass (fp32: three rows each)
+    constexpr int KS = 1024;
+    constexpr int EB = XT == SEEDMM_I8 ? 1 : 2;
+    constexpr int ROWB = KS * EB + 16;
+    __shared__ __align__(16) char xs[16 * ROWB];
+    __shared__ __align__(16) float sx[KS / GROUP][16];
+    __shared__ float red[4][16][17];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, q = lane >> 4;
+    const int64_t m0 = (int64_t)blockIdx.x * 16;
+    const int64_t row = m0 + r < a.M ? m0 + r : a.M - 1;
+    const int G = a.K / GROUP;
+    const uint32_t* wrow = a.w + row * (a.K / 8);
+    const int ntile = (a.N + TOK - 1) / TOK;
+
+    for (int tile = blockIdx.y; tile < ntile; tile += gridDim.y) {
+        const int n0 = tile * TOK;
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        for (int k0 = 0; k0 < a.K; k0 += KS) {
+            const int kn = min(KS, a.K - k0);
+            __syncthreads();
+            for (int u = tid; u < TOK * (KS / 8); u += 256) {
+                const int t = u / (KS / 8), kk = (u % (KS / 8)) * 8;
+                const bool ok = n0 + t < a.N && kk < kn;
+                const int64_t at = (int64_t)(n0 + t) * a.ldx + k0 + kk;
+                float sum = 0.f;
+                if constexpr (XT == SEEDMM_I8) {
+                    u32x2 v = {0u, 0u};
+                    if (ok) v = *(const u32x2*)((const int8_t*)a.x + at);
+                    int isum = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        isum += (int)(int8_t)(v[0] >> 8 * i) + (int)(int8_t)(v[1] >> 8 * i);
+                    sum = (float)isum;
+                    u32x2 p;
+                    p[0] = __builtin_amdgcn_perm(v[1], v[0], 0x06040200u);
+                    p[1] = __builtin_amdgcn_perm(v[1], v[0], 0x07050301u);
+                    *(u32x2*)(xs + t * ROWB + kk) = p;
+                } else if constexpr (XT == SEEDMM_BF16) {
+                    u32x4 v = {0u, 0u, 0u, 0u};
+                    if (ok) v = *(const u32x4*)((const uint16_t*)a.x + at);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        sum += __uint_as_float(v[i] << 16) + __uint_as_float(v[i] & 0xFFFF0000u);
+                    u32x4 p;
+                    p[0] = __builtin_amdgcn_perm(v[2], v[0], 0x05040100u);   // x0 x4
+                    p[1] = __builtin_amdgcn_perm(v[2], v[0], 0x07060302u);   // x1 x5
+                    p[2] = __builtin_amdgcn_perm(v[3], v[1], 0x05040100u);   // x2 x6
+                    p[3] = __builtin_amdgcn_perm(v[3], v[1], 0x07060302u);   // x3 x7
+                    *(u32x4*)(xs + t * ROWB + kk * 2) = p;
+                } else {
+                    f32x4 v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                    if (ok) {
+                        v[0] = *(const f32x4*)((const float*)a.x + at);
+                        v[1] = *(const f32x4*)((const float*)a.x + at + 4);
+                    }
+                    uint32_t pl[3][8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float f = v[i >> 2][i & 3];
+                        sum += f;
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) {
+                            pl[p][i] = __float_as_uint(f) & 0xFFFF0000u;
+                            f -= __uint_as_float(pl[p][i]);
+                        }
+                    }
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) {
+                        u32x4 o;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[i] = (pl[p][i] >> 16) | pl[p][i + 4];
+                        *(u32x4*)(xs + (3 * t + p) * ROWB + kk * 2) = o;
+                    }
+                }
+#pragma unroll
+                for (int d = 1; d < GROUP / 8; d *= 2) sum += __shfl_xor(sum, d);
+                if (kk % GROUP == 0) {
+                    if constexpr (XT == SEEDMM_F32) {
+                        sx[kk / GROUP][3 * t] = -16.f * sum;
+                        sx[kk / GROUP][3 * t + 1] = 0.f;
+                        sx[kk / GROUP][3 * t + 2] = 0.f;
+                        if (t == 0) sx[kk / GROUP][15] = 0.f;
+                    } else {
+                        sx[kk / GROUP][t] = XT == SEEDMM_I8 ? sum : -16.f * sum;
+                    }
+                }
+            }
+            if constexpr (XT == SEEDMM_F32) {   // the unused 16th row
+                for (int u = tid; u < KS / 8; u += 256) *(u32x4*)(xs + 15 * ROWB + u * 16) = u32x4{0u, 0u, 0u, 0u};
+            }
+            __syncthreads();
+            for (int st = wave * 128; st < kn; st += 512) {
+                uint32_t w[4] = {0u, 0u, 0u, 0u};
+                if (st + 32 * q < kn) {
+                    const u32x4 v = *(const u32x4*)(wrow + (k0 + st) / 8 + 4 * q);
+                    w[0] = v[0]; w[1] = v[1]; w[2] = v[2]; w[3] = v[3];
+                }
+                transpose_quarters(w);
+#pragma unroll
+                for (int g = 0; g < 128 / GROUP; ++g) {
+                    if (st + g * GROUP >= kn) break;   // uniform
+                    const int gl = st / GROUP + g;
+                    const f32x4 c = *(const f32x4*)&sx[gl][4 * q];
+                    const int64_t gi = row * G + k0 / GROUP + gl;
+                    const float s = load_scale<SF32>(a.s, gi), b = load_scale<SF32>(a.b, gi);
+                    f32x4 d;
+                    if constexpr (XT == SEEDMM_I8) {
+                        i32x4 di = {0, 0, 0, 0};
+#pragma unroll
+                        for (int j = g * (GROUP / 32); j < (g + 1) * (GROUP / 32); ++j) {
+                            const long xa = *(const long*)(xs + r * ROWB + st + 32 * j + 8 * q);
+                            di = __builtin_amdgcn_mfma_i32_16x16x32_i8(xa, codes_i8(w[j]), di, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) d[j] = (float)di[j];
+                    } else {
+                        d = c;
+#pragma unroll
+                        for (int j = g * (GROUP / 32); j < (g + 1) * (GROUP / 32); ++j) {
+                            const bf16x8 xa = *(const bf16x8*)(xs + r * ROWB + 2 * (st + 32 * j + 8 * q));
+                            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa, codes_bf16(w[j]), d, 0, 0, 0);
+                        }
+                    }
+                    const float bb = XT == SEEDMM_I8 ? b : -0.0625f * b;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        acc[j] = __builtin_fmaf(s, d[j], __builtin_fmaf(bb, c[j], acc[j]));
+                }
+            }
+        }
+        // D row 4 q + j = token row, column = weight row
+#pragma unroll
+        for (int j = 0; j < 4; ++j) red[wave][4 * q + j][r] = acc[j];
+        __syncthreads();
+        const int t = tid >> 4, c = tid & 15;
+        if (t < TOK && n0 + t < a.N && m0 + c < a.M) {
+            constexpr int PL = XT == SEEDMM_F32 ? 3 : 1;
+            float v = 0.f;
+#pragma unroll
+            for (int p = PL - 1; p >= 0; --p)
+                v += (red[0][PL * t + p][c] + red[1][PL * t + p][c]) +
+                     (red[2][PL * t + p][c] + red[3][PL * t + p][c]);
+            if constexpr (XT == SEEDMM_I8) v *= a.xs[n0 + t];
+            const int64_t o = (int64_t)(n0 + t) * a.ldy + m0 + c;
+            if (a.y_bf16) ((uint16_t*)a.y)[o] = f32_to_bf16(v);
+            else ((float*)a.y)[o] = v;
+        }
+    }
+}
+
+// K = 0: y = 0
+__global__ __launch_bounds__(256) void k_q4_zero(void* y, int y_bf16, int ldy, int M, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t o = i / M * ldy + i % M;
+        if (y_bf16) ((uint16_t*)y)[o] = 0;
+        else ((float*)y)[o] = 0.f;
+    }
+}
+
+// ----------------------------------------------------------------------------------
+// seedmm_add_norm.  r = x + delta in fp32; out = r rsqrt(mean r^2 + eps) w.  The 8-bit
+// scale is max |r w| times the row's factor over 127: one pass finds both statistics.
+// ----------------------------------------------------------------------------------
+struct NormArgs {
+    const void* x;
+    const void* d;       // null: none
+    const void* w;       // null: ones
+    void* res;           // null: not written
+    void* out;
+    float* scale;
+    int x_dt, d_dt, w_dt, out_dt;
+    int64_t ldx, ldd, ldr, ldo;
+    int N, H;
+    float eps;
+};
+
+__device__ __forceinline__ float load_el(const void* p, int dt, int64_t i) {
+    return dt == SEEDMM_F32 ? ((const float*)p)[i] : bf16_to_f32(((const uint16_t*)p)[i]);
+}
+
+__global__ __launch_bounds__(256) void k_add_norm(const NormArgs a) {
+    __shared__ float red[2][4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
+        float ss = 0.f, top = 0.f;
+        bool bad = false;
+        for (int h = threadIdx.x; h < a.H; h += 256) {
+            float r = load_el(a.x, a.x_dt, n * a.ldx + h);
+            if (a.d) r += load_el(a.d, a.d_dt, n * a.ldd + h);
+            const float v = a.w ? r * load_el(a.w, a.w_dt, h) : r;
+            ss = __builtin_fmaf(r, r, ss);
+            top = fmaxf(top, fabsf(v));
+            bad |= !(fabsf(v) < INFINITY);
+        }
+        if (bad) top = INFINITY;
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) {
+            ss += __shfl_xor(ss, o);
+            top = fmaxf(top, __shfl_xor(top, o));
+        }
+        if (lane == 0) { red[0][wave] = ss; red[1][wave] = top; }
+        __syncthreads();
+        ss = (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]);
+        top = fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3]));
+        __syncthreads();
+        const float f = 1.0f / sqrtf(ss / (float)a.H + a.eps);
+        float sc = 0.f, inv = 0.f;
+        if (a.out_dt == SEEDMM_I8) {
+            sc = fmaxf(top * f / 127.0f, 1.17549435e-38f);
+            // a row with an infinity or NaN: codes 0 and scale NaN
+            if (!(top * f < INFINITY)) sc = NAN;
+            inv = sc == sc ? 1.0f / sc : 0.f;
+            if (threadIdx.x == 0) a.scale[n] = sc;
+        }
+        for (int h = threadIdx.x; h < a.H; h += 256) {
+            float r = load_el(a.x, a.x_dt, n * a.ldx + h);
+            if (a.d) r += load_el(a.d, a.d_dt, n * a.ldd + h);
+            const float v = (a.w ? r * load_el(a.w, a.w_dt, h) : r) * f;
+            if (a.res) {
+                if (a.x_dt == SEEDMM_F32) ((float*)a.res)[n * a.ldr + h] = r;
+                else ((uint16_t*)a.res)[n * a.ldr + h] = f32_to_bf16(r);
+            }
+            if (a.out_dt == SEEDMM_I8) {
+                const float c = inv == 0.f ? 0.f : fminf(fmaxf(rintf(v * inv), -127.f), 127.f);
+                ((int8_t*)a.out)[n * a.ldo + h] = (int8_t)(int)c;
+            } else if (a.out_dt == SEEDMM_F32) {
+                ((float*)a.out)[n * a.ldo + h] = v;
+            } else {
+                ((uint16_t*)a.out)[n * a.ldo + h] = f32_to_bf16(v);
+            }
+        }
+    }
+}
+
+// ----------------------------------------------------------------------------------
+// seedmm_route.  One wave a token: the largest key of the E logits, top_k times.  A key
+// orders the eligible scores above 1, the ineligible experts (logit NaN or -inf) at 1 and
+// the chosen ones at 0; equal keys go to the lower expert.
+// ----------------------------------------------------------------------------------
+struct RouteArgs {
+    const void* lg;
+    const float* bias;
+    int32_t* ids;
+    float* w;
+    int64_t ldl;
+    int T, E, k, l_dt;
+};
+
+// order-preserving unsigned key of a float (-0 equals +0); -inf maps above 1
+__device__ __forceinline__ uint64_t key_of(double f) {
+    const uint64_t u = (uint64_t)__double_as_longlong(f + 0.0);
+    return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+
+template <int NPL, bool SIG>
+__global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
+    const int lane = threadIdx.x & 63;
+    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (t >= a.T) return;
+    uint64_t key[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const int e = i * 64 + lane;
+        key[i] = 0;
+        if (e < a.E) {
+            const float l = load_el(a.lg, a.l_dt, t * a.ldl + e);
+            double v = l;
+            if constexpr (SIG) {
+                v = 1.0 / (1.0 + exp(-(double)l));
+                if (a.bias) v += (double)a.bias[e];
+            }
+            key[i] = (l > -INFINITY && v > -INFINITY) ? key_of(v) : 1;
+        }
+    }
+    int mine = 0;         // lane s < k keeps slot s
+    bool elig = false;
+    for (int s = 0; s < a.k; ++s) {
+        uint64_t best = 0;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (key[i] > best) { best = key[i]; at = i; }
+        int e = at * 64 + lane;
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2) {
+            const uint64_t ob = __shfl_xor((unsigned long long)best, o);
+            const int oe = __shfl_xor(e, o);
+            if (ob > best || (ob == best && oe < e)) { best = ob; e = oe; }
+        }
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (i * 64 + lane == e) key[i] = 0;
+        if (lane == s) { mine = e; elig = best > 1; }
+    }
+    float l = -INFINITY;
+    if (lane < a.k && elig) l = load_el(a.lg, a.l_dt, t * a.ldl + mine);
+    float w;
+    if constexpr (SIG) {
+        w = (float)(1.0 / (1.0 + exp(-(double)l)));
+    } else {
+        float top = l;
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
+        w = l == top ? 1.0f : expf(l - top);
+    }
+    if (!elig || lane >= a.k) w = 0.f;
+    float sum = w;
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) sum += __shfl_xor(sum, o);
+    if (lane < a.k) {
+        a.ids[t * a.k + lane] = mine;
+        a.w[t * a.k + lane] = sum > 0.f ? w / sum : 0.f;
+    }
+}
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+int launch_status() { return hipGetLastError() == hipSuccess ? SEEDMM_OK : SEEDMM_EHIP; }
+size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
+
+template <int XT, bool SF32>
+void launch_q4(const Q4Args& a, int group, hipStream_t st) {
+    constexpr int TOK = XT == SEEDMM_F32 ? 5 : 16;
+    const int tiles = (a.N - 1) / TOK + 1;
+    const dim3 grid((unsigned)((a.M - 1) / 16 + 1), (unsigned)(tiles < 65535 ? tiles : 65535));
+    if (group == 32) hipLaunchKernelGGL((k_q4<XT, SF32, 32>), grid, dim3(256), 0, st, a);
+    else if (group == 64) hipLaunchKernelGGL((k_q4<XT, SF32, 64>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((k_q4<XT, SF32, 128>), grid, dim3(256), 0, st, a);
+}
+
+template <bool SIG>
+void launch_route(const RouteArgs& a, hipStream_t st) {
+    const dim3 grid((unsigned)((a.T - 1) / 4 + 1)), block(256);
+    if (a.E <= 64) hipLaunchKernelGGL((k_route<1, SIG>), grid, block, 0, st, a);
+    else if (a.E <= 128) hipLaunchKernelGGL((k_route<2, SIG>), grid, block, 0, st, a);
+    else if (a.E <= 256) hipLaunchKernelGGL((k_route<4, SIG>), grid, block, 0, st, a);
+    else if (a.E <= 512) hipLaunchKernelGGL((k_route<8, SIG>), grid, block, 0, st, a);
+    else if (a.E <= 1024) hipLaunchKernelGGL((k_route<16, SIG>), grid, block, 0, st, a);
+    else if (a.E <= 2048) hipLaunchKernelGGL((k_route<32, SIG>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((k_route<64, SIG>), grid, block, 0, st, a);
+}
+
+constexpr int kMaxDim = 1 << 30;   // row and column indices of a tile stay in 32 bits
+
+bool float_type(int dt) { return dt == SEEDMM_F32 || dt == SEEDMM_BF16; }
+
+}  // namespace
+
+extern "C" {
+
+int seedmm_q4_gemv(const uint32_t* weight, const void* scales, const void* biases, int s_dtype,
+                   int group, const void* x, int x_dtype, int ldx, const float* x_scale, void* y,
+                   int y_dtype, int ldy, int M, int K, int N, void* hip_stream) {
+    if (group != 32 && group != 64 && group != 128) return SEEDMM_EINVAL;
+    if (M < 0 || K < 0 || N < 0 || M > kMaxDim || K > kMaxDim || K % group != 0 || ldx < K || ldy < M) return SEEDMM_EINVAL;
+    if (!float_type(s_dtype) || !float_type(y_dtype)) return SEEDMM_EINVAL;
+    if (!float_type(x_dtype) && x_dtype != SEEDMM_I8) return SEEDMM_EINVAL;
+    if (M == 0 || N == 0) return SEEDMM_OK;
+    if (!y) return SEEDMM_EINVAL;
+    const int ymask = y_dtype == SEEDMM_F32 ? 3 : 1;
+    if ((uintptr_t)y & ymask) return SEEDMM_EALIGN;
+    hipStream_t st = (hipStream_t)hip_stream;
+    if (K == 0) {   // empty product: y = 0 (a kernel, not a memset node, under capture)
+        const int64_t n = (int64_t)N * M, blocks = (n + 255) / 256;
+        hipLaunchKernelGGL(k_q4_zero, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256),
+                           0, st, y, y_dtype == SEEDMM_BF16, ldy, M, n);
+        return launch_status();
+    }
+    if (!weight || !scales || !biases || !x) return SEEDMM_EINVAL;
+    if (x_dtype == SEEDMM_I8 ? !x_scale : x_scale != nullptr) return SEEDMM_EINVAL;
+    const int smask = s_dtype == SEEDMM_F32 ? 3 : 1;
+    if (!aligned16(weight) || !aligned16(x) || ((uintptr_t)scales & smask) ||
+        ((uintptr_t)biases & smask) || ((uintptr_t)x_scale & 3))
+        return SEEDMM_EALIGN;
+    const int per16 = x_dtype == SEEDMM_F32 ? 4 : x_dtype == SEEDMM_BF16 ? 8 : 16;
+    if (N > 1 && ldx % per16 != 0) return SEEDMM_EALIGN;
+    Q4Args a = {weight, scales, biases, x, x_scale, y, M, K, N, ldx, ldy, y_dtype == SEEDMM_BF16};
+    const bool sf = s_dtype == SEEDMM_F32;
+    if (x_dtype == SEEDMM_F32) sf ? launch_q4<SEEDMM_F32, true>(a, group, st) : launch_q4<SEEDMM_F32, false>(a, group, st);
+    else if (x_dtype == SEEDMM_BF16) sf ? launch_q4<SEEDMM_BF16, true>(a, group, st) : launch_q4<SEEDMM_BF16, false>(a, group, st);
+    else sf ? launch_q4<SEEDMM_I8, true>(a, group, st) : launch_q4<SEEDMM_I8, false>(a, group, st);
+    return launch_status();
+}
+
+int seedmm_add_norm(const void* x, int x_dtype, int64_t ldx, const void* delta, int delta_dtype,
+                    int64_t ldd, const void* weight, int w_dtype, float eps, void* residual,
+                    int64_t ldr, void* out, int out_dtype, int64_t ldo, float* scale, int N, int H,
+                    void* hip_stream) {
+    if (N < 0 || H < 0 || !(eps >= 0.f) || !(eps < INFINITY)) return SEEDMM_EINVAL;
+    if (!float_type(x_dtype) || (delta && !float_type(delta_dtype)) || (weight && !float_type(w_dtype)))
+        return SEEDMM_EINVAL;
+    if (!float_type(out_dtype) && out_dtype != SEEDMM_I8) return SEEDMM_EINVAL;
+    if (ldx < H || (delta && ldd < H) || (residual && ldr < H) || ldo < H) return SEEDMM_EINVAL;
+    if ((out_dtype == SEEDMM_I8) != (scale != nullptr) && N > 0 && H > 0) return SEEDMM_EINVAL;
+    if (N == 0 || H == 0) return SEEDMM_OK;
+    if (!x || !out) return SEEDMM_EINVAL;
+    auto off = [](const void* p, int dt) { return ((uintptr_t)p & (dt == SEEDMM_F32 ? 3 : dt == SEEDMM_BF16 ? 1 : 0)) != 0; };
+    if (off(x, x_dtype) || (delta && off(delta, delta_dtype)) || (weight && off(weight, w_dtype)) ||
+        (residual && off(residual, x_dtype)) || off(out, out_dtype) || ((uintptr_t)scale & 3))
+        return SEEDMM_EALIGN;
+    NormArgs a = {x, delta, weight, residual, out, scale, x_dtype, delta_dtype, w_dtype, out_dtype,
+                  ldx, ldd, ldr, ldo, N, H, eps};
+    hipLaunchKernelGGL(k_add_norm, dim3((unsigned)N), dim3(256), 0, (hipStream_t)hip_stream, a);
+    return launch_status();
+}
+
+int seedmm_route(const void* logits, int l_dtype, int64_t ldl, const float* bias, int score, int T,
+                 int E, int top_k, int32_t* ids, float* w, void* hip_stream) {
+    if (T < 0 || E < 1 || E > 4096 || top_k < 1 || top_k > E || top_k > 64) return SEEDMM_EINVAL;
+    if ((int64_t)T * top_k > 0x7FFFFFFF || ldl < E || !float_type(l_dtype)) return SEEDMM_EINVAL;
+    if (score != SEEDMM_SOFTMAX && score != SEEDMM_SIGMOID) return SEEDMM_EINVAL;
+    if (bias && score == SEEDMM_SOFTMAX) return SEEDMM_EINVAL;
+    if (T == 0) return SEEDMM_OK;
+    if (!logits || !ids || !w) return SEEDMM_EINVAL;
+    if (((uintptr_t)logits & (l_dtype == SEEDMM_F32 ? 3 : 1)) || ((uintptr_t)bias & 3) ||
+        ((uintptr_t)ids & 3) || ((uintptr_t)w & 3))
+        return SEEDMM_EALIGN;
+    RouteArgs a = {logits, bias, ids, w, ldl, T, E, top_k, l_dtype};
+    if (score == SEEDMM_SIGMOID) launch_route<true>(a, (hipStream_t)hip_stream);
+    else launch_route<false>(a, (hipStream_t)hip_stream);
+    return launch_status();
+}
+
+// Scratch of one block call: the normed rows, the logits, the routing (if the caller keeps
+// none) and the routed layer's own workspace.
+static bool block_layout(const seedmm_block* b, int T, size_t at[5]) {
+    if (!b || T < 0 || b->E < 1 || b->H < 0) return false;
+    const size_t layer = seedmm_moe_workspace_bytes(T, b->top_k, b->E, b->H, b->I);
+    if (layer == 0) return false;
+    at[0] = align_up((size_t)T * (size_t)b->H * 2);
+    at[1] = at[0] + align_up((size_t)T * (size_t)b->E * 4);
+    at[2] = at[1] + align_up((size_t)T * (size_t)b->top_k * 4);
+    at[3] = at[2] + align_up((size_t)T * (size_t)b->top_k * 4);
+    at[4] = at[3] + layer;
+    return true;
+}
+
+size_t seedmm_moe_block_workspace_bytes(const seedmm_block* block, int T) {
+    size_t at[5];
+    return block_layout(block, T, at) ? at[4] : 0;
+}
+
+int seedmm_moe_block(const seedmm_block* block, void* r, int r_dtype, const void* delta,
+                     int delta_dtype, float* y, int32_t* ids, float* w, int T, void* workspace,
+                     size_t workspace_bytes, void* hip_stream, const seedmm_side* side) {
+    size_t at[5];
+    if (!block || T < 0) return SEEDMM_EINVAL;
+    const seedmm_block& b = *block;
+    if (!block_layout(block, T, at)) return SEEDMM_EINVAL;
+    // every check of the four calls before the first launch: the routed layer's and the
+    // choice's with an empty batch, whose checks stop before any launch
+    if (int e = seedmm_moe_ex(nullptr, nullptr, 0, b.top_k, nullptr, nullptr, b.E, b.H, b.I, b.P,
+                              b.p4mask, b.gate, b.up, b.down, nullptr, 0, hip_stream, nullptr))
+        return e;
+    if (int e = seedmm_route(nullptr, SEEDMM_F32, b.E, b.router_bias, b.score, 0, b.E, b.top_k,
+                             nullptr, nullptr, hip_stream))
+        return e;
+    if (int e = seedmm_q4_gemv(nullptr, nullptr, nullptr, b.router_dtype, b.group, nullptr,
+                               SEEDMM_BF16, b.H, nullptr, nullptr, SEEDMM_F32, b.E, b.E, b.H, 0,
+                               hip_stream))
+        return e;
+    if (int e = seedmm_add_norm(nullptr, r_dtype, b.H, delta, delta_dtype, b.H, b.norm_weight,
+                                b.norm_dtype, b.eps, nullptr, b.H, nullptr, SEEDMM_BF16, b.H,
+                                nullptr, 0, b.H, hip_stream))
+        return e;
+    if (T == 0) return SEEDMM_OK;
+    const seedmm_mat* mats[3] = {&b.gate, &b.up, &b.down};
+    for (const seedmm_mat* m : mats)
+        if (!m->seeds || !m->coefs || !m->codes || !m->exp_bias) return SEEDMM_EINVAL;
+    if (!r || !y || !b.router_weight || !b.router_scales || !b.router_biases) return SEEDMM_EINVAL;
+    if (side && side->stream && (!side->fork || !side->join || side->stream == hip_stream))
+        return SEEDMM_EINVAL;
+    if (!aligned16(r) || !aligned16(delta) || !aligned16(y) || !aligned16(b.norm_weight) ||
+        !aligned16(b.router_weight) || !aligned16(b.router_scales) || !aligned16(b.router_biases) ||
+        ((uintptr_t)b.router_bias & 3) || ((uintptr_t)ids & 3) || ((uintptr_t)w & 3))
+        return SEEDMM_EALIGN;
+    if (!workspace || workspace_bytes < at[4]) return SEEDMM_EWORKSPACE;
+    if (!aligned16(workspace)) return SEEDMM_EALIGN;
+    char* ws = (char*)workspace;
+    float* logits = (float*)(ws + at[0]);
+    if (!ids) ids = (int32_t*)(ws + at[1]);
+    if (!w) w = (float*)(ws + at[2]);
+    int e = seedmm_add_norm(r, r_dtype, b.H, delta, delta_dtype, b.H, b.norm_weight, b.norm_dtype,
+                            b.eps, delta ? r : nullptr, b.H, ws, SEEDMM_BF16, b.H, nullptr, T, b.H,
+                            hip_stream);
+    if (!e)
+        e = seedmm_q4_gemv(b.router_weight, b.router_scales, b.router_biases, b.router_dtype, b.group,
+                           ws, SEEDMM_BF16, b.H, nullptr, logits, SEEDMM_F32, b.E, b.E, b.H, T,
+                           hip_stream);
+    if (!e)
+        e = seedmm_route(logits, SEEDMM_F32, b.E, b.router_bias, b.score, T, b.E, b.top_k, ids, w,
+                         hip_stream);
+    if (!e)
+        e = seedmm_moe_ex(ids, w, T, b.top_k, ws, y, b.E, b.H, b.I, b.P, b.p4mask, b.gate, b.up,
+                          b.down, ws + at[3], at[4] - at[3], hip_stream, side);
+    return e;
+}
+
+}  // extern "C"

@@ -17,7 +17,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libseedmm.so")
 
 OK, EINVAL, EALIGN, EWORKSPACE, EHIP, ECAPACITY, ESCRATCH = 0, -1, -2, -3, -4, -5, -6
-F32, BF16 = 0, 1
+F32, BF16, I8 = 0, 1, 2
+SOFTMAX, SIGMOID = 0, 1
 NOALLOC_SCRATCH_BYTES = 8 << 20      # SEEDMM_NOALLOC_SCRATCH_BYTES of include/seedmm.h
 
 
@@ -30,6 +31,14 @@ class SeedmmError(RuntimeError):
 class SeedMat(ctypes.Structure):
     _fields_ = [("seeds", ctypes.c_void_p), ("coefs", ctypes.c_void_p),
                 ("codes", ctypes.c_void_p), ("exp_bias", ctypes.c_void_p)]
+
+
+class SeedBlock(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("norm_weight", "router_weight", "router_scales",
+                                                "router_biases", "router_bias", "p4mask")]
+                + [(n, SeedMat) for n in ("gate", "up", "down")] + [("eps", ctypes.c_float)]
+                + [(n, ctypes.c_int) for n in ("norm_dtype", "router_dtype", "group", "score",
+                                               "top_k", "E", "H", "I", "P")])
 
 
 class SeedSide(ctypes.Structure):
@@ -75,6 +84,16 @@ def _load():
     L.seedmm_cache_plan.argtypes = [p, p, i32, i32, p, p]
     L.seedmm_cache_moe.argtypes = [p, p, p, p, i32, i32, p, p, p, sz, p]
     L.seedmm_cache_stats.argtypes = [p, p]
+    i64 = ctypes.c_int64
+    L.seedmm_q4_gemv.argtypes = [p, p, p, i32, i32, p, i32, i32, p, p, i32, i32, i32, i32, i32, p]
+    L.seedmm_add_norm.argtypes = [p, i32, i64, p, i32, i64, p, i32, ctypes.c_float, p, i64, p, i32,
+                                  i64, p, i32, i32, p]
+    L.seedmm_route.argtypes = [p, i32, i64, p, i32, i32, i32, i32, p, p, p]
+    blk = ctypes.POINTER(SeedBlock)
+    L.seedmm_moe_block_workspace_bytes.restype = sz
+    L.seedmm_moe_block_workspace_bytes.argtypes = [blk, i32]
+    L.seedmm_moe_block.argtypes = [blk, p, i32, p, i32, p, p, p, i32, p, sz, p,
+                                   ctypes.POINTER(SeedSide)]
     L.seedmm_strerror.restype = ctypes.c_char_p
     L.seedmm_strerror.argtypes = [i32]
     L.seedmm_version.restype = i32
@@ -83,7 +102,8 @@ def _load():
                  "seedmm_search",
                  "seedmm_search_prepare", "seedmm_moe_mixed",
                  "seedmm_cache_init", "seedmm_cache_reset", "seedmm_cache_plan",
-                 "seedmm_cache_moe", "seedmm_cache_stats"):
+                 "seedmm_cache_moe", "seedmm_cache_stats", "seedmm_q4_gemv", "seedmm_add_norm",
+                 "seedmm_route", "seedmm_moe_block"):
         getattr(L, name).restype = i32
     return L
 
@@ -97,7 +117,9 @@ EXPORTS = ("seedmm_gemv", "seedmm_gemv_ex", "seedmm_reconstruct", "seedmm_moe_di
            "seedmm_search_prepare", "seedmm_cache_record_layout", "seedmm_cache_state_bytes",
            "seedmm_cache_device_bytes",
            "seedmm_cache_init", "seedmm_cache_reset", "seedmm_cache_plan", "seedmm_cache_moe",
-           "seedmm_cache_stats", "seedmm_strerror", "seedmm_version")
+           "seedmm_cache_stats", "seedmm_q4_gemv", "seedmm_add_norm", "seedmm_route",
+           "seedmm_moe_block_workspace_bytes", "seedmm_moe_block", "seedmm_strerror",
+           "seedmm_version")
 
 
 def lib():
@@ -579,3 +601,249 @@ class ExpertCache:
         out = (ctypes.c_uint64 * 5)()
         _check(_lib.seedmm_cache_stats(self.handle, out), "seedmm_cache_stats")
         return dict(zip(("calls", "uses", "hits", "misses", "bytes"), (int(v) for v in out)))
+
+
+# ---- dense operators around the routed layer -----------------------------------------
+
+_FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
+_ROWS = {torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8}
+
+
+def _row_tensor(t, types, name, dev=None):
+    """(dtype code, rows, columns, leading dimension) of a row-major GPU tensor [N][C] or
+    [C] whose rows may be apart (last dimension contiguous)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    code = types.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be one of {[str(d) for d in types]}, got {t.dtype}")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} is on another device")
+    shape = t.shape
+    if len(shape) == 2:
+        n, c = shape
+        st = t.stride()
+        ld = st[0] if n > 1 else c
+        if (c > 1 and st[1] != 1) or ld < c:
+            raise ValueError(f"{name} must be row-major with contiguous, distinct rows")
+        return code, n, c, ld
+    if len(shape) == 1 and (shape[0] <= 1 or t.stride(0) == 1):
+        return code, 1, shape[0], shape[0]
+    raise ValueError(f"{name} must be a row-major [N][C] or a contiguous [C] tensor")
+
+
+def _flat(t, types, n, name, dev):
+    """dtype code of a contiguous GPU tensor of at least n elements."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    code = types.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be one of {[str(d) for d in types]}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() < n:
+        raise ValueError(f"{name} has {t.numel()} elements, {n} needed")
+    return code
+
+
+_U32 = {torch.uint32: 0}
+_INT32 = {torch.int32: 0}
+_FP32 = {torch.float32: F32}
+
+
+def _launch(dev, stream, what, fn, *args):
+    """One library call on `stream` (None: the current stream of device `dev`), with that
+    device current."""
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError("the stream belongs to another device than the tensors")
+        handle = stream.cuda_stream
+    else:
+        handle = _current_stream_handle(dev)
+    if dev == torch.cuda.current_device():
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, handle)
+    if status != OK:
+        raise SeedmmError(status, what)
+
+
+def _check_q4(mat, M, K, group, dev):
+    if group not in (32, 64, 128) or K % group:
+        raise ValueError(f"K = {K} must be a multiple of the group, and the group 32, 64 or 128")
+    _flat(mat["weight"], _U32, M * (K // 8), "weight", dev)
+    sd = _flat(mat["scales"], _FLOATS, M * (K // group), "scales", dev)
+    if _flat(mat["biases"], _FLOATS, M * (K // group), "biases", dev) != sd:
+        raise TypeError("scales and biases must have one type")
+    return sd
+
+
+def q4_gemv(mat: dict, x: torch.Tensor, M: int, K: int, group: int = 64, x_scale=None, y=None,
+            y_dtype=torch.float32, stream=None):
+    """y = x W^T for W in affine 4 bits (seedmm_q4_gemv).  mat: {"weight": uint32 [M*K/8],
+    "scales", "biases": fp32 or bf16 [M*K/group]}; x fp32, bf16 or int8 [N][K] (or [K]),
+    int8 rows with x_scale fp32 [N]; y [N][M] (or [M]) fp32 or bf16."""
+    xd, N, cols, ldx = _row_tensor(x, _ROWS, "x")
+    dev = x.get_device()
+    if cols < K:
+        raise ValueError(f"x rows hold {cols} elements, K = {K}")
+    sd = _check_q4(mat, M, K, group, dev)
+    if xd == I8:
+        _flat(x_scale, _FP32, N, "x_scale", dev)
+    elif x_scale is not None:
+        raise ValueError("x_scale goes with int8 activations")
+    if y is None:
+        with _on(stream):
+            y = torch.empty((N, M) if x.dim() == 2 else (M,), dtype=y_dtype, device=x.device)
+    yd, yn, yc, ldy = _row_tensor(y, _FLOATS, "y", dev)
+    if yn < N or yc < M:
+        raise ValueError(f"y must hold [{N}][{M}]")
+    _launch(dev, stream, "seedmm_q4_gemv", _lib.seedmm_q4_gemv, mat["weight"].data_ptr(),
+            mat["scales"].data_ptr(), mat["biases"].data_ptr(), sd, group, x.data_ptr(), xd, ldx,
+            None if x_scale is None else x_scale.data_ptr(), y.data_ptr(), yd, ldy, M, K, N)
+    return y
+
+
+def add_norm(x: torch.Tensor, weight=None, delta=None, eps: float = 1e-6,
+             out_dtype=torch.bfloat16, residual=None, out=None, scale=None, stream=None):
+    """(out, scale, residual): r = x + delta and its root-mean-square norm (seedmm_add_norm).
+    x fp32 or bf16 [N][H] (or [H]); delta fp32 or bf16 of x's shape or None; weight fp32 or
+    bf16 [H] or None; out of out_dtype (float32, bfloat16, or int8 with scale fp32 [N]; scale
+    is None otherwise).  residual: r in x's type (pass x itself to update it in place); x if
+    there is no delta and none is asked for."""
+    xd, N, H, ldx = _row_tensor(x, _FLOATS, "x")
+    dev = x.get_device()
+    dd, ldd, wd, ldr = F32, H, F32, H
+    if delta is not None:
+        dd, dn, dc, ldd = _row_tensor(delta, _FLOATS, "delta", dev)
+        if dn != N or dc != H:
+            raise ValueError("delta must have x's shape")
+    if weight is not None:
+        wd = _flat(weight, _FLOATS, H, "weight", dev)
+    with _on(stream):
+        if out is None:
+            out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
+        od, on, oc, ldo = _row_tensor(out, _ROWS, "out", dev)
+        if od == I8 and scale is None:
+            scale = torch.empty(N, dtype=torch.float32, device=x.device)
+        if delta is not None and residual is None:
+            residual = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if on != N or oc != H:
+        raise ValueError("out must have x's shape")
+    if od == I8:
+        _flat(scale, _FP32, N, "scale", dev)
+    elif scale is not None:
+        raise ValueError("scale goes with an int8 out")
+    if residual is not None:
+        rd, rn, rc, ldr = _row_tensor(residual, _FLOATS, "residual", dev)
+        if rd != xd or rn != N or rc != H:
+            raise ValueError("residual must have x's shape and type")
+    _launch(dev, stream, "seedmm_add_norm", _lib.seedmm_add_norm, x.data_ptr(), xd, ldx,
+            None if delta is None else delta.data_ptr(), dd, ldd,
+            None if weight is None else weight.data_ptr(), wd, eps,
+            None if residual is None else residual.data_ptr(), ldr, out.data_ptr(), od, ldo,
+            None if scale is None else scale.data_ptr(), N, H)
+    return out, scale, x if residual is None else residual
+
+
+_SCORES = {"softmax": SOFTMAX, "sigmoid": SIGMOID}
+
+
+def route(logits: torch.Tensor, top_k: int, bias=None, score: str = "softmax", ids=None, w=None,
+          stream=None):
+    """(ids int32 [T][top_k], w fp32 [T][top_k]) of router logits fp32 or bf16 [T][E]
+    (seedmm_route): the routing that moe() takes.  score "softmax", or "sigmoid" with an
+    optional fp32 selection bias [E]."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T][E]")
+    ld_, T, E, ldl = _row_tensor(logits, _FLOATS, "logits")
+    dev = logits.get_device()
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}")
+    if bias is not None:
+        _flat(bias, _FP32, E, "bias", dev)
+    if not 1 <= top_k <= min(E, 64):
+        raise ValueError(f"top_k = {top_k} must be in [1, min(E, 64)], E = {E}")
+    if ids is None or w is None:
+        with _on(stream):
+            if ids is None:
+                ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+            if w is None:
+                w = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+    _flat(ids, _INT32, T * top_k, "ids", dev)
+    _flat(w, _FP32, T * top_k, "w", dev)
+    _launch(dev, stream, "seedmm_route", _lib.seedmm_route, logits.data_ptr(), ld_, ldl,
+            None if bias is None else bias.data_ptr(), _SCORES[score], T, E, top_k, ids.data_ptr(),
+            w.data_ptr())
+    return ids, w
+
+
+class MoeBlock:
+    """One routed layer with its norm and router (seedmm_moe_block): holds the layer's
+    tensors.  gate/up/down as for moe(); router: an [E][H] affine 4-bit matrix as for
+    q4_gemv(); norm_weight fp32 or bf16 [H] or None.  P = 3 or 4, or Ps (a P per expert)
+    for mixed packs."""
+
+    def __init__(self, E, H, I, P, top_k, gate, up, down, router, group=64, norm_weight=None,
+                 eps=1e-6, score="softmax", router_bias=None, Ps=None):
+        dev = gate["seeds"].get_device()
+        for name, m, (M, K) in (("gate", gate, (I, H)), ("up", up, (I, H)), ("down", down, (H, I))):
+            _seedmat(m)
+            _check_streams(m, E, M, K, Ps if Ps is not None else P, name)
+            for part in ("seeds", "coefs", "codes", "exp_bias"):
+                if m[part].get_device() != dev:
+                    raise ValueError(f"{name}.{part} is on another device")
+        if score not in _SCORES:
+            raise ValueError(f"score must be one of {sorted(_SCORES)}")
+        rd = _check_q4(router, E, H, group, dev)
+        nd = F32 if norm_weight is None else _flat(norm_weight, _FLOATS, H, "norm_weight", dev)
+        if router_bias is not None:
+            _flat(router_bias, _FP32, E, "router_bias", dev)
+        self.p4mask = None if Ps is None else p4_mask(Ps, gate["seeds"].device)
+        self.E, self.H, self.top_k, self.device = E, H, top_k, gate["seeds"].device
+        self._keep = (gate, up, down, router, norm_weight, router_bias)
+        ptr = lambda t: None if t is None else t.data_ptr()
+        self._c = SeedBlock(ptr(norm_weight), ptr(router["weight"]), ptr(router["scales"]),
+                            ptr(router["biases"]), ptr(router_bias), ptr(self.p4mask),
+                            _seedmat(gate), _seedmat(up), _seedmat(down), eps, nd, rd, group,
+                            _SCORES[score], top_k, E, H, I, 0 if Ps is not None else P)
+        if self.workspace_bytes(1) == 0:
+            raise SeedmmError(EINVAL, "seedmm_moe_block sizes")
+
+    def workspace_bytes(self, T: int) -> int:
+        return int(_lib.seedmm_moe_block_workspace_bytes(ctypes.byref(self._c), T))
+
+    def moe(self, r, delta=None, y=None, ids=None, w=None, workspace=None, stream=None, side=None):
+        """y fp32 [T][H] of the residual stream r (fp32 or bf16 [T][H], contiguous), which
+        delta (fp32 or bf16 [T][H]) is added to in place first.  ids, w: optional tensors
+        that receive the routing."""
+        dev = self.device.index
+        rd = _flat(r, _FLOATS, 0, "r", dev)
+        if r.dim() != 2 or r.shape[1] != self.H:
+            raise ValueError(f"r must be [T][{self.H}]")
+        T = r.shape[0]
+        dd = F32 if delta is None else _flat(delta, _FLOATS, T * self.H, "delta", dev)
+        with _on(stream):
+            if y is None:
+                y = torch.empty((T, self.H), dtype=torch.float32, device=r.device)
+            if workspace is None:
+                workspace = torch.empty(self.workspace_bytes(T), dtype=torch.uint8, device=r.device)
+        _flat(y, _FP32, T * self.H, "y", dev)
+        if ids is not None:
+            _flat(ids, _INT32, T * self.top_k, "ids", dev)
+        if w is not None:
+            _flat(w, _FP32, T * self.top_k, "w", dev)
+        if workspace.get_device() != dev:
+            raise ValueError("the workspace is on another device")
+        sd = None if side is None else ctypes.byref(side.c())
+        ptr = lambda t: None if t is None else t.data_ptr()
+
+        def call(*a):
+            return _lib.seedmm_moe_block(*a, sd)
+        _launch(dev, stream, "seedmm_moe_block", call, ctypes.byref(self._c), r.data_ptr(), rd,
+                ptr(delta), dd, y.data_ptr(), ptr(ids), ptr(w), T, workspace.data_ptr(),
+                workspace.numel() * workspace.element_size())
+        return y
