@@ -26,9 +26,7 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float f) { return __builtin_bit_
 // Both sums are exact products: a code q is an integer of 4 bits, so it enters the matrix
 // instruction without rounding, and the scale multiplies the group's fp32 sum afterwards
 // (a weight s q + b is never rounded to the activation's type).
-//   bf16 x: 16 + q is the bf16 with bits 0x4180 | q << 3, one shift and one and-or for two
-//     codes; the group's accumulator starts at -16 X, which takes the 16 away again (the
-//     offset is at most twice a code, so the cancellation costs one bit of the fp32 sum).
+//   bf16 x: a code is an integer below 16, exact in bf16.
 //   fp32 x: split into three bf16 of 8 bits each (truncated, so the split is exact), three
 //     rows of the same instruction.
 //   int8 x: the integer instruction; D is exact.
@@ -61,177 +59,247 @@ __device__ __forceinline__ void transpose_quarters(uint32_t (&w)[4]) {
     w[0] = c[0]; w[1] = c[1]; w[2] = d[0]; w[3] = d[1];
 }
 
-// 8 codes -> bf16 16 + q in the order 0 4 1 5 2 6 3 7
+// 8 codes -> bf16 in the order 0 2 4 6 1 3 5 7.  A byte 0 .. 15 read as an 8-bit float
+// (e4m3) is code * 2^-9 exactly, subnormal or not, so the pair conversion with scale 2^9
+// gives the integers: 7 instructions for 8 codes.
 __device__ __forceinline__ bf16x8 codes_bf16(uint32_t w) {
+    const uint32_t a = w & 0x0F0F0F0Fu, b = (w >> 4) & 0x0F0F0F0Fu;
     u32x4 v;
-    v[0] = ((w << 3) & 0x00780078u) | 0x41804180u;
-    v[1] = ((w >> 1) & 0x00780078u) | 0x41804180u;
-    v[2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
-    v[3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
+    v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 512.0f, false));
+    v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 512.0f, true));
+    v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.0f, false));
+    v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.0f, true));
     return __builtin_bit_cast(bf16x8, v);
 }
 
-// 8 codes -> bytes in the order 0 2 4 6 1 3 5 7
-__device__ __forceinline__ long codes_i8(uint32_t w) {
-    u32x2 v;
-    v[0] = w & 0x0F0F0F0Fu;
-    v[1] = (w >> 4) & 0x0F0F0F0Fu;
-    return __builtin_bit_cast(long, v);
+// 8 codes -> bytes in the same order
+__device__ __forceinline__ u32x2 codes_i8(uint32_t w) {
+    return u32x2{w & 0x0F0F0F0Fu, (w >> 4) & 0x0F0F0F0Fu};
 }
 
-// 16 weight rows a workgroup, its four waves take 128-column steps in turn; the activation
-// rows of a slab of columns are staged in LDS in the operands' order.
-template <int XT, bool SF32, int GROUP>
-__global__ __launch_bounds__(256) void k_q4(const Q4Args a) {
-    constexpr int TOK = XT == SEEDMM_F32 ? 5 : 16;   // tokens a pass (fp32: three rows each)
-    constexpr int KS = 1024;
+// NG consecutive scales from index i of which the first nv exist (the others read as 0).
+// Whole runs are one load of 2-byte (bf16) or 4-byte (fp32) alignment.
+template <bool SF32, int NG>
+struct Scales {
+    uint32_t u[SF32 ? NG : (NG + 1) / 2];
+    __device__ __forceinline__ void load(const void* p, int64_t i, int nv) {
+        const char* at = (const char*)p + i * (SF32 ? 4 : 2);
+        if (nv >= NG) {
+            if constexpr (!SF32 && NG == 1) u[0] = *(const uint16_t*)at;
+            else __builtin_memcpy(u, at, sizeof(u));
+        } else {
+#pragma unroll
+            for (int g = 0; g < (int)(sizeof(u) / 4); ++g) u[g] = 0;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                if (g < nv) {
+                    if constexpr (SF32) u[g] = ((const uint32_t*)at)[g];
+                    else u[g / 2] |= (uint32_t)((const uint16_t*)at)[g] << (16 * (g & 1));
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ float get(int g) const {
+        if constexpr (SF32) return __uint_as_float(u[g]);
+        else return __uint_as_float((g & 1) ? u[g / 2] & 0xFFFF0000u : u[g / 2] << 16);
+    }
+};
+
+// Stages 8 columns of activation row `src` (or zeros) in the operands' order: XT rows `dst`
+// apart by `rowb` (fp32: three).  Returns the columns' sum.
+template <int XT>
+__device__ __forceinline__ float stage8(const void* x, int64_t at, bool ok, char* dst, int rowb) {
+    float sum = 0.f;
+    if constexpr (XT == SEEDMM_I8) {
+        u32x2 v = {0u, 0u};
+        if (ok) v = *(const u32x2*)((const int8_t*)x + at);
+        int isum = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) isum += (int)(int8_t)(v[0] >> 8 * i) + (int)(int8_t)(v[1] >> 8 * i);
+        sum = (float)isum;
+        u32x2 p;
+        p[0] = __builtin_amdgcn_perm(v[1], v[0], 0x06040200u);
+        p[1] = __builtin_amdgcn_perm(v[1], v[0], 0x07050301u);
+        *(u32x2*)dst = p;
+    } else if constexpr (XT == SEEDMM_BF16) {
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (ok) v = *(const u32x4*)((const uint16_t*)x + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum += __uint_as_float(v[i] << 16) + __uint_as_float(v[i] & 0xFFFF0000u);
+        u32x4 p;
+        p[0] = __builtin_amdgcn_perm(v[1], v[0], 0x05040100u);   // x0 x2
+        p[1] = __builtin_amdgcn_perm(v[3], v[2], 0x05040100u);   // x4 x6
+        p[2] = __builtin_amdgcn_perm(v[1], v[0], 0x07060302u);   // x1 x3
+        p[3] = __builtin_amdgcn_perm(v[3], v[2], 0x07060302u);   // x5 x7
+        *(u32x4*)dst = p;
+    } else {
+        f32x4 v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        if (ok) {
+            v[0] = *(const f32x4*)((const float*)x + at);
+            v[1] = *(const f32x4*)((const float*)x + at + 4);
+        }
+        uint32_t pl[3][8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float f = v[i >> 2][i & 3];
+            sum += f;
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+                pl[p][i] = __float_as_uint(f) & 0xFFFF0000u;
+                f -= __uint_as_float(pl[p][i]);
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            u32x4 o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = i < 2 ? 4 * i : 4 * i - 7;   // 0 4 1 5: first of the pair (e, e + 2)
+                o[i] = (pl[p][e] >> 16) | pl[p][e + 2];
+            }
+            *(u32x4*)(dst + p * rowb) = o;
+        }
+    }
+    return sum;
+}
+
+// A few tokens.  A wave takes 16 weight rows; KW waves of a workgroup share a row tile and
+// take its 128-column steps in turn, PF steps loaded ahead of the ones multiplied, the first
+// before the activations are staged.  The D tile of 16x16x32 instructions has a row a
+// token: up to 4 activation rows sit in D rows 0, 4, 8, 12 (JN = 1), so each lane scales
+// one value a group instead of four.
+template <int XT, bool SF32, int GROUP, int JN, int WAVES, int KW>
+__global__ __launch_bounds__(WAVES * 64) void k_q4(const Q4Args a, int slab) {
+    constexpr int PL = XT == SEEDMM_F32 ? 3 : 1;       // operand rows a token
     constexpr int EB = XT == SEEDMM_I8 ? 1 : 2;
-    constexpr int ROWB = KS * EB + 16;
-    __shared__ __align__(16) char xs[16 * ROWB];
-    __shared__ __align__(16) float sx[KS / GROUP][16];
-    __shared__ float red[4][16][17];
+    constexpr int NG = 128 / GROUP;
+    constexpr int PF = KW >= 16 ? 1 : 4;
+    constexpr int RW = WAVES / KW;
+    constexpr int SXW = JN == 1 ? 4 : 16;
+    __shared__ float red[KW][RW][JN * 4][17];
+    extern __shared__ __align__(16) char lds[];
+    const int rowb = slab * EB + 16;
+    float* sx = (float*)lds;                                     // [slab / GROUP][SXW]
+    char* xs = lds + (size_t)(slab / GROUP) * SXW * 4;           // [rows][rowb]
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int kw = wave % KW, rw = wave / KW;
     const int r = lane & 15, q = lane >> 4;
-    const int64_t m0 = (int64_t)blockIdx.x * 16;
+    const int rows = a.N * PL;                                   // <= 4 (JN = 1) or 16
+    const int64_t m0 = ((int64_t)blockIdx.x * RW + rw) * 16;
     const int64_t row = m0 + r < a.M ? m0 + r : a.M - 1;
     const int G = a.K / GROUP;
-    const uint32_t* wrow = a.w + row * (a.K / 8);
-    const int ntile = (a.N + TOK - 1) / TOK;
+    const uint32_t* wrow = a.w + row * (a.K / 8) + 4 * q;
+    const int xrow = JN == 1 ? min(r >> 2, rows - 1) : min(r, rows - 1);
+    const char* xl = xs + xrow * rowb + (XT == SEEDMM_I8 ? 8 : 16) * q;
 
-    for (int tile = blockIdx.y; tile < ntile; tile += gridDim.y) {
-        const int n0 = tile * TOK;
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-        for (int k0 = 0; k0 < a.K; k0 += KS) {
-            const int kn = min(KS, a.K - k0);
-            __syncthreads();
-            for (int u = tid; u < TOK * (KS / 8); u += 256) {
-                const int t = u / (KS / 8), kk = (u % (KS / 8)) * 8;
-                const bool ok = n0 + t < a.N && kk < kn;
-                const int64_t at = (int64_t)(n0 + t) * a.ldx + k0 + kk;
-                float sum = 0.f;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int k0 = 0; k0 < a.K; k0 += slab) {
+        const int kn = min(slab, a.K - k0);
+        const int ns = (kn + 127) / 128;
+        u32x4 w[2][PF];
+        Scales<SF32, NG> ss[2][PF], bs[2][PF];
+        auto load = [&](int buf, int it) {
+#pragma unroll
+            for (int p = 0; p < PF; ++p) {
+                const int st = (it + p) * KW + kw;
+                if (st < ns) {
+                    w[buf][p] = u32x4{0u, 0u, 0u, 0u};
+                    if (st * 128 + 32 * q < kn) w[buf][p] = *(const u32x4*)(wrow + (k0 + st * 128) / 8);
+                    const int g = k0 / GROUP + st * NG;
+                    ss[buf][p].load(a.s, row * G + g, G - g);
+                    bs[buf][p].load(a.b, row * G + g, G - g);
+                }
+            }
+        };
+        load(0, 0);
+        if (k0) __syncthreads();
+        const int per_row = slab / 8;
+        for (int u = tid; u < a.N * per_row; u += WAVES * 64) {
+            const int t = u / per_row, kk = (u - t * per_row) * 8;
+            float sum = stage8<XT>(a.x, (int64_t)t * a.ldx + k0 + kk, kk < kn,
+                                   xs + t * PL * rowb + kk * EB, rowb);
+#pragma unroll
+            for (int d = 1; d < GROUP / 8; d *= 2) sum += __shfl_xor(sum, d);
+            if (kk % GROUP == 0) {
+#pragma unroll
+                for (int p = 0; p < PL; ++p) sx[kk / GROUP * SXW + t * PL + p] = p ? 0.f : sum;
+            }
+        }
+        __syncthreads();
+        auto step = [&](const u32x4& wv, const Scales<SF32, NG>& sv, const Scales<SF32, NG>& bv, int st) {
+            uint32_t c[4] = {wv[0], wv[1], wv[2], wv[3]};
+            transpose_quarters(c);
+            const char* xp = xl + st * 128 * EB;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const int gl = st * NG + g;
+                f32x4 d = {0.f, 0.f, 0.f, 0.f};
                 if constexpr (XT == SEEDMM_I8) {
-                    u32x2 v = {0u, 0u};
-                    if (ok) v = *(const u32x2*)((const int8_t*)a.x + at);
-                    int isum = 0;
+                    i32x4 di = {0, 0, 0, 0};
+                    if constexpr (GROUP == 32) {
+                        const long xa = *(const long*)(xp + 32 * g);
+                        di = __builtin_amdgcn_mfma_i32_16x16x32_i8(xa, __builtin_bit_cast(long, codes_i8(c[g])), di, 0, 0, 0);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        isum += (int)(int8_t)(v[0] >> 8 * i) + (int)(int8_t)(v[1] >> 8 * i);
-                    sum = (float)isum;
-                    u32x2 p;
-                    p[0] = __builtin_amdgcn_perm(v[1], v[0], 0x06040200u);
-                    p[1] = __builtin_amdgcn_perm(v[1], v[0], 0x07050301u);
-                    *(u32x2*)(xs + t * ROWB + kk) = p;
-                } else if constexpr (XT == SEEDMM_BF16) {
-                    u32x4 v = {0u, 0u, 0u, 0u};
-                    if (ok) v = *(const u32x4*)((const uint16_t*)a.x + at);
+                        for (int j = g * (GROUP / 32); j < (g + 1) * (GROUP / 32); j += 2) {
+                            const u32x2 x0 = *(const u32x2*)(xp + 32 * j), x1 = *(const u32x2*)(xp + 32 * j + 32);
+                            const u32x2 c0 = codes_i8(c[j]), c1 = codes_i8(c[j + 1]);
+                            di = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                                i32x4{(int)x0[0], (int)x0[1], (int)x1[0], (int)x1[1]},
+                                i32x4{(int)c0[0], (int)c0[1], (int)c1[0], (int)c1[1]}, di, 0, 0, 0);
+                        }
+                    }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        sum += __uint_as_float(v[i] << 16) + __uint_as_float(v[i] & 0xFFFF0000u);
-                    u32x4 p;
-                    p[0] = __builtin_amdgcn_perm(v[2], v[0], 0x05040100u);   // x0 x4
-                    p[1] = __builtin_amdgcn_perm(v[2], v[0], 0x07060302u);   // x1 x5
-                    p[2] = __builtin_amdgcn_perm(v[3], v[1], 0x05040100u);   // x2 x6
-                    p[3] = __builtin_amdgcn_perm(v[3], v[1], 0x07060302u);   // x3 x7
-                    *(u32x4*)(xs + t * ROWB + kk * 2) = p;
+                    for (int j = 0; j < JN; ++j) d[j] = (float)di[j];
                 } else {
-                    f32x4 v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                    if (ok) {
-                        v[0] = *(const f32x4*)((const float*)a.x + at);
-                        v[1] = *(const f32x4*)((const float*)a.x + at + 4);
-                    }
-                    uint32_t pl[3][8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float f = v[i >> 2][i & 3];
-                        sum += f;
-#pragma unroll
-                        for (int p = 0; p < 3; ++p) {
-                            pl[p][i] = __float_as_uint(f) & 0xFFFF0000u;
-                            f -= __uint_as_float(pl[p][i]);
-                        }
-                    }
-#pragma unroll
-                    for (int p = 0; p < 3; ++p) {
-                        u32x4 o;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[i] = (pl[p][i] >> 16) | pl[p][i + 4];
-                        *(u32x4*)(xs + (3 * t + p) * ROWB + kk * 2) = o;
-                    }
+                    for (int j = g * (GROUP / 32); j < (g + 1) * (GROUP / 32); ++j)
+                        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(*(const bf16x8*)(xp + 64 * j), codes_bf16(c[j]), d, 0, 0, 0);
                 }
-#pragma unroll
-                for (int d = 1; d < GROUP / 8; d *= 2) sum += __shfl_xor(sum, d);
-                if (kk % GROUP == 0) {
-                    if constexpr (XT == SEEDMM_F32) {
-                        sx[kk / GROUP][3 * t] = -16.f * sum;
-                        sx[kk / GROUP][3 * t + 1] = 0.f;
-                        sx[kk / GROUP][3 * t + 2] = 0.f;
-                        if (t == 0) sx[kk / GROUP][15] = 0.f;
-                    } else {
-                        sx[kk / GROUP][t] = XT == SEEDMM_I8 ? sum : -16.f * sum;
-                    }
-                }
-            }
-            if constexpr (XT == SEEDMM_F32) {   // the unused 16th row
-                for (int u = tid; u < KS / 8; u += 256) *(u32x4*)(xs + 15 * ROWB + u * 16) = u32x4{0u, 0u, 0u, 0u};
-            }
-            __syncthreads();
-            for (int st = wave * 128; st < kn; st += 512) {
-                uint32_t w[4] = {0u, 0u, 0u, 0u};
-                if (st + 32 * q < kn) {
-                    const u32x4 v = *(const u32x4*)(wrow + (k0 + st) / 8 + 4 * q);
-                    w[0] = v[0]; w[1] = v[1]; w[2] = v[2]; w[3] = v[3];
-                }
-                transpose_quarters(w);
-#pragma unroll
-                for (int g = 0; g < 128 / GROUP; ++g) {
-                    if (st + g * GROUP >= kn) break;   // uniform
-                    const int gl = st / GROUP + g;
-                    const f32x4 c = *(const f32x4*)&sx[gl][4 * q];
-                    const int64_t gi = row * G + k0 / GROUP + gl;
-                    const float s = load_scale<SF32>(a.s, gi), b = load_scale<SF32>(a.b, gi);
-                    f32x4 d;
-                    if constexpr (XT == SEEDMM_I8) {
-                        i32x4 di = {0, 0, 0, 0};
-#pragma unroll
-                        for (int j = g * (GROUP / 32); j < (g + 1) * (GROUP / 32); ++j) {
-                            const long xa = *(const long*)(xs + r * ROWB + st + 32 * j + 8 * q);
-                            di = __builtin_amdgcn_mfma_i32_16x16x32_i8(xa, codes_i8(w[j]), di, 0, 0, 0);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) d[j] = (float)di[j];
-                    } else {
-                        d = c;
-#pragma unroll
-                        for (int j = g * (GROUP / 32); j < (g + 1) * (GROUP / 32); ++j) {
-                            const bf16x8 xa = *(const bf16x8*)(xs + r * ROWB + 2 * (st + 32 * j + 8 * q));
-                            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa, codes_bf16(w[j]), d, 0, 0, 0);
-                        }
-                    }
-                    const float bb = XT == SEEDMM_I8 ? b : -0.0625f * b;
+                const float s = sv.get(g), b = bv.get(g);
+                if constexpr (JN == 1) {
+                    acc[0] = __builtin_fmaf(s, d[0], __builtin_fmaf(b, sx[gl * 4 + q], acc[0]));
+                } else {
+                    const f32x4 X = *(const f32x4*)&sx[gl * 16 + 4 * q];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        acc[j] = __builtin_fmaf(s, d[j], __builtin_fmaf(bb, c[j], acc[j]));
+                        acc[j] = __builtin_fmaf(s, d[j], __builtin_fmaf(b, X[j], acc[j]));
                 }
             }
-        }
-        // D row 4 q + j = token row, column = weight row
+        };
+        const int nit = (ns - kw + KW - 1) / KW;      // this wave's steps
+        for (int it = 0; it < nit; it += 2 * PF) {
+            load(1, it + PF);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) red[wave][4 * q + j][r] = acc[j];
-        __syncthreads();
-        const int t = tid >> 4, c = tid & 15;
-        if (t < TOK && n0 + t < a.N && m0 + c < a.M) {
-            constexpr int PL = XT == SEEDMM_F32 ? 3 : 1;
-            float v = 0.f;
+            for (int p = 0; p < PF; ++p)
+                if (it + p < nit) step(w[0][p], ss[0][p], bs[0][p], (it + p) * KW + kw);
+            load(0, it + 2 * PF);
 #pragma unroll
-            for (int p = PL - 1; p >= 0; --p)
-                v += (red[0][PL * t + p][c] + red[1][PL * t + p][c]) +
-                     (red[2][PL * t + p][c] + red[3][PL * t + p][c]);
-            if constexpr (XT == SEEDMM_I8) v *= a.xs[n0 + t];
-            const int64_t o = (int64_t)(n0 + t) * a.ldy + m0 + c;
-            if (a.y_bf16) ((uint16_t*)a.y)[o] = f32_to_bf16(v);
-            else ((float*)a.y)[o] = v;
+            for (int p = 0; p < PF; ++p)
+                if (it + PF + p < nit) step(w[1][p], ss[1][p], bs[1][p], (it + PF + p) * KW + kw);
         }
+    }
+    // the KW partial tiles meet in LDS in their order; D column = weight row
+#pragma unroll
+    for (int j = 0; j < JN; ++j) red[kw][rw][JN * q + j][r] = acc[j];
+    __syncthreads();
+    for (int u = tid; u < RW * 16 * a.N; u += WAVES * 64) {
+        const int c = u & 15, h = (u >> 4) % RW, t = (u >> 4) / RW;
+        const int64_t m = ((int64_t)blockIdx.x * RW + h) * 16 + c;
+        if (m >= a.M) continue;
+        float v = 0.f;
+#pragma unroll
+        for (int p = PL - 1; p >= 0; --p) {
+            float e = red[0][h][t * PL + p][c];
+#pragma unroll
+            for (int k = 1; k < KW; ++k) e += red[k][h][t * PL + p][c];
+            v += e;
+        }
+        if constexpr (XT == SEEDMM_I8) v *= a.xs[t];
+        const int64_t o = (int64_t)t * a.ldy + m;
+        if (a.y_bf16) ((uint16_t*)a.y)[o] = f32_to_bf16(v);
+        else ((float*)a.y)[o] = v;
     }
 }
 
@@ -400,18 +468,55 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
     }
 }
 
+constexpr int kMaxDim = 1 << 30;   // row and column indices of a tile stay in 32 bits
+constexpr int kQ4Lds = 44 * 1024;   // staged activations of a workgroup
+
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 int launch_status() { return hipGetLastError() == hipSuccess ? SEEDMM_OK : SEEDMM_EHIP; }
 size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
 
+template <int XT, bool SF32, int GROUP, int JN, int WAVES, int KW>
+void launch_q4_kw(const Q4Args& a, hipStream_t st) {
+    constexpr int EB = XT == SEEDMM_I8 ? 1 : 2, PL = XT == SEEDMM_F32 ? 3 : 1;
+    // the activation rows of a slab of columns in LDS, all columns if they fit
+    const int rows = a.N * PL;
+    const int per = 128 * EB * rows + 128 / GROUP * (JN == 1 ? 4 : 16) * 4;   // bytes of 128 columns
+    int slab = (kQ4Lds - rows * 16) / per * 128;
+    const int kround = (a.K + 127) / 128 * 128;
+    if (slab > kround) slab = kround;
+    const size_t lds = (size_t)slab / 128 * per + rows * 16;
+    const int64_t tiles = ((int64_t)a.M + 15) / 16;
+    const dim3 grid((unsigned)((tiles + WAVES / KW - 1) / (WAVES / KW)));
+    hipLaunchKernelGGL((k_q4<XT, SF32, GROUP, JN, WAVES, KW>), grid, dim3(WAVES * 64), lds, st, a, slab);
+}
+
+template <int XT, bool SF32, int GROUP, int JN>
+void launch_q4_jn(const Q4Args& a, hipStream_t st) {
+    const int64_t tiles = ((int64_t)a.M + 15) / 16;
+    if (tiles >= 4096) launch_q4_kw<XT, SF32, GROUP, JN, 8, 1>(a, st);
+    else if (tiles >= 256) launch_q4_kw<XT, SF32, GROUP, JN, 8, 4>(a, st);
+    else launch_q4_kw<XT, SF32, GROUP, JN, 16, 16>(a, st);
+}
+
+template <int XT, bool SF32, int GROUP>
+void launch_q4_group(const Q4Args& all, hipStream_t st) {
+    constexpr int PL = XT == SEEDMM_F32 ? 3 : 1, TOK = 16 / PL;
+    Q4Args a = all;
+    for (int64_t n0 = 0; n0 < all.N; n0 += TOK) {
+        a.N = (int)(all.N - n0 < TOK ? all.N - n0 : TOK);
+        a.x = (const char*)all.x + n0 * all.ldx * (XT == SEEDMM_F32 ? 4 : XT == SEEDMM_BF16 ? 2 : 1);
+        a.xs = all.xs ? all.xs + n0 : nullptr;
+        a.y = (char*)all.y + n0 * all.ldy * (all.y_bf16 ? 2 : 4);
+        if (a.N * PL <= 4) launch_q4_jn<XT, SF32, GROUP, 1>(a, st);
+        else launch_q4_jn<XT, SF32, GROUP, 4>(a, st);
+    }
+}
+
 template <int XT, bool SF32>
 void launch_q4(const Q4Args& a, int group, hipStream_t st) {
-    constexpr int TOK = XT == SEEDMM_F32 ? 5 : 16;
-    const int tiles = (a.N - 1) / TOK + 1;
-    const dim3 grid((unsigned)((a.M - 1) / 16 + 1), (unsigned)(tiles < 65535 ? tiles : 65535));
-    if (group == 32) hipLaunchKernelGGL((k_q4<XT, SF32, 32>), grid, dim3(256), 0, st, a);
-    else if (group == 64) hipLaunchKernelGGL((k_q4<XT, SF32, 64>), grid, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((k_q4<XT, SF32, 128>), grid, dim3(256), 0, st, a);
+    if (group == 32) launch_q4_group<XT, SF32, 32>(a, st);
+    else if (group == 64) launch_q4_group<XT, SF32, 64>(a, st);
+    else launch_q4_group<XT, SF32, 128>(a, st);
 }
 
 template <bool SIG>
@@ -425,8 +530,6 @@ void launch_route(const RouteArgs& a, hipStream_t st) {
     else if (a.E <= 2048) hipLaunchKernelGGL((k_route<32, SIG>), grid, block, 0, st, a);
     else hipLaunchKernelGGL((k_route<64, SIG>), grid, block, 0, st, a);
 }
-
-constexpr int kMaxDim = 1 << 30;   // row and column indices of a tile stay in 32 bits
 
 bool float_type(int dt) { return dt == SEEDMM_F32 || dt == SEEDMM_BF16; }
 
