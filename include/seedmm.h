@@ -418,13 +418,21 @@ int seedmm_cache_stats(const seedmm_cache *cache, uint64_t out[5]);
  *   without finite meaning and leaves the other rows alone.
  * Errors: SEEDMM_EINVAL (null pointer, M, K or N < 0, M or K above 2^30, another group,
  * K % group != 0, ldx < K, ldy < M, bad dtype, x_scale missing or given without
- * SEEDMM_I8), SEEDMM_EALIGN (weight or x not 16-byte aligned, ldx not a multiple of 16
- * bytes where N > 1, another pointer not aligned to its type), SEEDMM_EHIP.  M = 0 or
+ * SEEDMM_I8), SEEDMM_EALIGN (weight, x or the workspace not 16-byte aligned, ldx not a
+ * multiple of 16 bytes where N > 1, another pointer not aligned to its type),
+ * SEEDMM_EWORKSPACE (workspace missing or smaller than seedmm_q4_workspace_bytes), SEEDMM_EHIP.  M = 0 or
  * N = 0 is an empty success; K = 0 writes zeros.
  */
 int seedmm_q4_gemv(const uint32_t *weight, const void *scales, const void *biases, int s_dtype,
                    int group, const void *x, int x_dtype, int ldx, const float *x_scale, void *y,
-                   int y_dtype, int ldy, int M, int K, int N, void *hip_stream);
+                   int y_dtype, int ldy, int M, int K, int N, void *workspace,
+                   size_t workspace_bytes, void *hip_stream);
+/* Bytes of device scratch (16-byte aligned, contents need not be initialised) that a product
+ * of these sizes needs: 0 for few rows (up to 16; 5 with fp32 x), where workspace may be
+ * NULL; else the activation rows in the operands' order and, where K is split over
+ * workgroups, the partial sums.  0 on bad arguments.  Calls that overlap in time use
+ * different workspaces. */
+size_t seedmm_q4_workspace_bytes(int x_dtype, int group, int M, int K, int N);
 
 /*
  * seedmm_add_norm -- the residual's addition and the root-mean-square norm before a layer

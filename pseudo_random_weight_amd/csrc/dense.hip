@@ -108,7 +108,7 @@ struct Scales {
 // Stages 8 columns of activation row `src` (or zeros) in the operands' order: XT rows `dst`
 // apart by `rowb` (fp32: three).  Returns the columns' sum.
 template <int XT>
-__device__ __forceinline__ float stage8(const void* x, int64_t at, bool ok, char* dst, int rowb) {
+__device__ __forceinline__ float stage8(const void* x, int64_t at, bool ok, char* dst, int64_t rowb) {
     float sum = 0.f;
     if constexpr (XT == SEEDMM_I8) {
         u32x2 v = {0u, 0u};
@@ -303,6 +303,287 @@ __global__ __launch_bounds__(WAVES * 64) void k_q4(const Q4Args a, int slab) {
     }
 }
 
+// Many tokens.  k_q4_rows writes the activations once as bf16 rows in the operands' order
+// (fp32: three planes) and the groups' sums as three bf16 planes; k_q4_wide multiplies tiles
+// of them with the codes on 32x32x16 instructions.
+//
+// The bias term is a product of its own over the groups, sum_g b[m][g] X[n][g]: it starts
+// the accumulators with matrix instructions (3 for 16 groups; 6 with fp32 biases, which
+// are split as well), so the vector units only add s D, one fma an element a 64 columns.
+//
+// A wave holds MT tiles of 32 weight rows by TT tiles of 32 tokens.  Lane r + 32 h loads the
+// 16 bytes of row r that hold columns 32 h .. 32 h + 31 of a 64-column step: word j is its
+// operand of instruction j with no exchange (groups of 32: after one swap of the halves).
+struct Q4Wide {
+    Q4Args a;
+    const uint16_t* xp;   // [PL][N][Kp] rows in the operands' order, zero past K
+    const uint16_t* xg;   // [3][N][Gp] group sums, zero past K / group
+    float* part;          // [S][N][M] partial sums (S = 1: null)
+    int Kp, Gp, ksplit;   // columns a split
+    int tn, tm;           // tiles of tokens and of weight rows
+};
+
+__device__ __forceinline__ void split3(float f, uint32_t (&p)[3]) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        p[i] = __float_as_uint(f) & 0xFFFF0000u;
+        f -= __uint_as_float(p[i]);
+    }
+}
+
+// One thread a run of 8 columns; the lanes of a group add their sums.
+template <int XT, int GROUP>
+__global__ __launch_bounds__(256) void k_q4_rows(const Q4Args a, uint16_t* xp, uint16_t* xg, int Kp, int Gp) {
+    const int per = Kp / 8;
+    const int64_t all = (int64_t)a.N * per, plane = (int64_t)a.N * Kp, gplane = (int64_t)a.N * Gp;
+    // a wave's 64 runs start at a multiple of the group's, and so do the rows
+    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < (all + 63) / 64 * 64; u += (int64_t)gridDim.x * 256) {
+        const int64_t n = u / per;
+        const int kk = (int)(u - n * per) * 8;
+        const bool in = u < all, ok = in && kk < a.K;
+        float sum = 0.f;
+        if (in) {
+            if constexpr (XT == SEEDMM_I8) {
+                u32x2 v = {0u, 0u};
+                if (ok) v = *(const u32x2*)((const int8_t*)a.x + n * a.ldx + kk);
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    f[i] = (float)(int8_t)(v[i >> 2] >> 8 * (i & 3));
+                    sum += f[i];
+                }
+                u32x4 o;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = i < 2 ? 4 * i : 4 * i - 7;
+                    o[i] = (__float_as_uint(f[e]) >> 16) | (__float_as_uint(f[e + 2]) & 0xFFFF0000u);
+                }
+                *(u32x4*)(xp + n * Kp + kk) = o;
+            } else {
+                sum = stage8<XT>(a.x, n * a.ldx + kk, ok, (char*)(xp + n * Kp + kk), plane * 2);
+            }
+        }
+#pragma unroll
+        for (int d = 1; d < GROUP / 8; d *= 2) sum += __shfl_xor(sum, d);
+        if (ok && kk % GROUP == 0) {
+            uint32_t p[3];
+            split3(sum, p);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) xg[i * gplane + n * Gp + kk / GROUP] = (uint16_t)(p[i] >> 16);
+        }
+        // the padding groups of a row
+        const int G = a.K / GROUP;
+        if (in)
+            for (int g = G + kk / 8; g < Gp; g += per)
+#pragma unroll
+                for (int i = 0; i < 3; ++i) xg[i * gplane + n * Gp + g] = 0;
+    }
+}
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+template <int PL, bool SF32, int GROUP, int TT, int MT, int WN, int WM>
+__global__ __launch_bounds__(WN * WM * 64) void k_q4_wide(const Q4Wide c) {
+    constexpr int BT = 32 * TT * WN, BM = 32 * MT * WM, NTH = 64 * WN * WM;
+    constexpr int NST = PL * BT * 8 / NTH;      // 16-byte pieces of a step a thread stages
+    static_assert(PL * BT * 8 % NTH == 0, "whole pieces");
+    __shared__ u32x4 xs[2][PL * BT * 8];
+    const Q4Args& a = c.a;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave / WM, wm = wave % WM;
+    const int r = lane & 31, h = lane >> 5;
+    // workgroups of one XCD (every eighth) take neighbouring tiles, token tiles first
+    const int total = c.tn * c.tm;
+    int id = blockIdx.x;
+    if (total % 8 == 0) id = (id & 7) * (total >> 3) + (id >> 3);
+    const int n0 = (id % c.tn) * BT;
+    const int64_t m0 = (int64_t)(id / c.tn) * BM + 32 * MT * wm;
+    const int kb = blockIdx.y * c.ksplit, ke = min(a.K, kb + c.ksplit);
+    const int G = a.K / GROUP;
+
+    // staging: piece u = 16 bytes `u & 7` of tile row u >> 3, kept at slot (u & 7) ^ (row & 7)
+    int64_t src[NST];
+    int dst[NST];
+#pragma unroll
+    for (int i = 0; i < NST; ++i) {
+        const int u = i * NTH + tid, row = u >> 3, p = row / BT, t = row % BT;
+        src[i] = ((int64_t)p * a.N + min(n0 + t, a.N - 1)) * c.Kp + 8 * (u & 7);
+        dst[i] = row * 8 + ((u & 7) ^ (row & 7));
+    }
+    u32x4 stage[NST];
+    auto fetch = [&](int k) {
+#pragma unroll
+        for (int i = 0; i < NST; ++i) stage[i] = *(const u32x4*)(c.xp + src[i] + k);
+    };
+    auto put = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < NST; ++i) xs[buf][dst[i]] = stage[i];
+    };
+    int64_t row[MT];
+    const uint32_t* wrow[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        row[mt] = m0 + 32 * mt + r < a.M ? m0 + 32 * mt + r : a.M - 1;
+        wrow[mt] = a.w + row[mt] * (a.K / 8) + 4 * h;
+    }
+    constexpr int NG = GROUP == 32 ? 2 : 1;      // groups a step
+    u32x4 wv[MT];
+    float sv[MT][NG];
+    auto weights = [&](int k) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            wv[mt] = u32x4{0u, 0u, 0u, 0u};
+            if (k + 32 * h < a.K) wv[mt] = *(const u32x4*)(wrow[mt] + k / 8);
+            Scales<SF32, NG> s;
+            s.load(a.s, row[mt] * G + k / GROUP, G - k / GROUP);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) sv[mt][g] = s.get(g);
+        }
+    };
+
+    f32x16 acc[TT][MT];
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[tt][mt][i] = 0.f;
+    fetch(kb);
+    weights(kb);
+    if (blockIdx.y == 0) {      // bias term
+        for (int g0 = 0; g0 < G; g0 += 16) {
+            const int gl = g0 + 8 * h;
+            bf16x8 bb[MT][SF32 ? 3 : 1];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                Scales<SF32, 8> b;
+                b.load(a.b, row[mt] * G + min(gl, G), G - min(gl, G));
+                if constexpr (SF32) {
+                    uint32_t p[8][3];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) split3(b.get(i), p[i]);
+#pragma unroll
+                    for (int q = 0; q < 3; ++q) {
+                        u32x4 o;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[i] = (p[2 * i][q] >> 16) | p[2 * i + 1][q];
+                        bb[mt][q] = __builtin_bit_cast(bf16x8, o);
+                    }
+                } else {
+                    bb[mt][0] = __builtin_bit_cast(bf16x8, u32x4{b.u[0], b.u[1], b.u[2], b.u[3]});
+                }
+            }
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) {
+                const int n = min(n0 + 32 * (TT * wn + tt) + r, a.N - 1);
+                bf16x8 xa[3];
+#pragma unroll
+                for (int p = 0; p < 3; ++p)
+                    xa[p] = *(const bf16x8*)(c.xg + ((int64_t)p * a.N + n) * c.Gp + gl);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int q = 0; q < (SF32 ? 3 : 1); ++q)
+#pragma unroll
+                        for (int p = 0; p + q < 3; ++p)
+                            acc[tt][mt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[p], bb[mt][q], acc[tt][mt], 0, 0, 0);
+            }
+        }
+    }
+    put(0);
+    __syncthreads();
+
+    int buf = 0;
+    for (int k = kb; k < ke; k += 64, buf ^= 1) {
+        const bool more = k + 64 < ke;
+        bf16x8 bq[MT][4];
+        float s[MT][NG];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            uint32_t w[4] = {wv[mt][0], wv[mt][1], wv[mt][2], wv[mt][3]};
+            if constexpr (GROUP == 32) {
+                auto x = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+                auto y = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+                w[0] = x[0]; w[2] = x[1]; w[1] = y[0]; w[3] = y[1];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) bq[mt][j] = codes_bf16(w[j]);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) s[mt][g] = sv[mt][g];
+        }
+        if (more) {
+            fetch(k + 64);
+            weights(k + 64);
+        }
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) {
+            const int t = 32 * (TT * wn + tt) + r;
+            bf16x8 xa[PL][4];
+#pragma unroll
+            for (int p = 0; p < PL; ++p)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int ch = GROUP == 32 ? 4 * (j >> 1) + 2 * h + (j & 1) : 4 * h + j;
+                    xa[p][j] = __builtin_bit_cast(bf16x8, xs[buf][(p * BT + t) * 8 + (ch ^ (t & 7))]);
+                }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    f32x16 d = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int p = 0; p < PL; ++p)
+#pragma unroll
+                        for (int j = g * 4 / NG; j < (g + 1) * 4 / NG; ++j)
+                            d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[p][j], bq[mt][j], d, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        acc[tt][mt][i] = __builtin_fmaf(s[mt][g], d[i], acc[tt][mt][i]);
+                }
+            }
+        }
+        if (more) put(buf ^ 1);
+        __syncthreads();
+    }
+
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int n = n0 + 32 * (TT * wn + tt) + 8 * (i >> 2) + 4 * h + (i & 3);
+            if (n >= a.N) continue;
+            const float xsc = a.xs && !c.part ? a.xs[n] : 1.0f;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const int64_t m = m0 + 32 * mt + r;
+                if (m >= a.M) continue;
+                const float v = acc[tt][mt][i] * xsc;
+                if (c.part) {
+                    c.part[((int64_t)blockIdx.y * a.N + n) * a.M + m] = v;
+                } else {
+                    const int64_t o = (int64_t)n * a.ldy + m;
+                    if (a.y_bf16) ((uint16_t*)a.y)[o] = f32_to_bf16(v);
+                    else ((float*)a.y)[o] = v;
+                }
+            }
+        }
+}
+
+// y = the S partial sums in their order
+__global__ __launch_bounds__(256) void k_q4_join(const Q4Args a, const float* part, int S) {
+    const int64_t n = (int64_t)a.N * a.M;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        float v = part[i];
+        for (int s = 1; s < S; ++s) v += part[s * n + i];
+        const int64_t t = i / a.M, m = i - t * a.M;
+        if (a.xs) v *= a.xs[t];
+        const int64_t o = t * a.ldy + m;
+        if (a.y_bf16) ((uint16_t*)a.y)[o] = f32_to_bf16(v);
+        else ((float*)a.y)[o] = v;
+    }
+}
+
 // K = 0: y = 0
 __global__ __launch_bounds__(256) void k_q4_zero(void* y, int y_bf16, int ldy, int M, int64_t n) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
@@ -471,9 +752,9 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
 constexpr int kMaxDim = 1 << 30;   // row and column indices of a tile stay in 32 bits
 constexpr int kQ4Lds = 44 * 1024;   // staged activations of a workgroup
 
+size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 int launch_status() { return hipGetLastError() == hipSuccess ? SEEDMM_OK : SEEDMM_EHIP; }
-size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
 
 template <int XT, bool SF32, int GROUP, int JN, int WAVES, int KW>
 void launch_q4_kw(const Q4Args& a, hipStream_t st) {
@@ -498,25 +779,73 @@ void launch_q4_jn(const Q4Args& a, hipStream_t st) {
     else launch_q4_kw<XT, SF32, GROUP, JN, 16, 16>(a, st);
 }
 
+// The plan of a product with many tokens: what its workspace holds.
+struct Q4Plan {
+    bool wide;
+    int Kp, Gp, S, ksplit, cfg, tn, tm;
+    size_t xg, part, total;
+};
+
+Q4Plan q4_plan(int x_dtype, int group, int M, int K, int N) {
+    Q4Plan p = {};
+    const int PL = x_dtype == SEEDMM_F32 ? 3 : 1;
+    p.wide = (int64_t)N * PL > 16 && M > 0 && K > 0;
+    if (!p.wide) return p;
+    p.Kp = (K + 63) / 64 * 64;
+    p.Gp = (K / group + 15) / 16 * 16;
+    // tiles: 256 x 256 where they fill the chip, else 64 x 128 with K split until they do
+    const int64_t big = ((int64_t)(N + 255) / 256) * ((M + 255) / 256);
+    p.cfg = PL == 1 && big >= 256 ? 1 : 0;
+    const int BT = p.cfg ? 256 : 64, BM = p.cfg ? 256 : 128;
+    p.tn = (int)(((int64_t)N + BT - 1) / BT);
+    p.tm = (int)(((int64_t)M + BM - 1) / BM);
+    const int steps = (K + 127) / 128;
+    int64_t S = p.cfg ? 1 : 512 / ((int64_t)p.tn * p.tm);
+    if (S > steps / 2) S = steps / 2;
+    if (S > 16) S = 16;
+    if (S < 1) S = 1;
+    const int per = (int)((steps + S - 1) / S);
+    p.ksplit = per * 128;
+    p.S = (steps + per - 1) / per;
+    p.xg = align_up((size_t)PL * (size_t)N * (size_t)p.Kp * 2);
+    p.part = p.xg + align_up((size_t)3 * (size_t)N * (size_t)p.Gp * 2);
+    p.total = p.part + (p.S > 1 ? align_up((size_t)p.S * (size_t)N * (size_t)M * 4) : 0);
+    return p;
+}
+
 template <int XT, bool SF32, int GROUP>
-void launch_q4_group(const Q4Args& all, hipStream_t st) {
-    constexpr int PL = XT == SEEDMM_F32 ? 3 : 1, TOK = 16 / PL;
-    Q4Args a = all;
-    for (int64_t n0 = 0; n0 < all.N; n0 += TOK) {
-        a.N = (int)(all.N - n0 < TOK ? all.N - n0 : TOK);
-        a.x = (const char*)all.x + n0 * all.ldx * (XT == SEEDMM_F32 ? 4 : XT == SEEDMM_BF16 ? 2 : 1);
-        a.xs = all.xs ? all.xs + n0 : nullptr;
-        a.y = (char*)all.y + n0 * all.ldy * (all.y_bf16 ? 2 : 4);
+void launch_q4_group(const Q4Args& a, const Q4Plan& p, void* ws, hipStream_t st) {
+    constexpr int PL = XT == SEEDMM_F32 ? 3 : 1;
+    if (!p.wide) {
         if (a.N * PL <= 4) launch_q4_jn<XT, SF32, GROUP, 1>(a, st);
         else launch_q4_jn<XT, SF32, GROUP, 4>(a, st);
+        return;
+    }
+    uint16_t* xp = (uint16_t*)ws;
+    uint16_t* xg = (uint16_t*)((char*)ws + p.xg);
+    const int64_t runs = (int64_t)a.N * (p.Kp / 8), blocks = (runs + 255) / 256;
+    hipLaunchKernelGGL((k_q4_rows<XT, GROUP>), dim3((unsigned)(blocks < 65536 ? blocks : 65536)),
+                       dim3(256), 0, st, a, xp, xg, p.Kp, p.Gp);
+    Q4Wide c = {a, xp, xg, p.S > 1 ? (float*)((char*)ws + p.part) : nullptr, p.Kp, p.Gp, p.ksplit, p.tn, p.tm};
+    const dim3 grid((unsigned)((int64_t)p.tn * p.tm), (unsigned)p.S);
+    if constexpr (PL == 1) {
+        if (p.cfg) hipLaunchKernelGGL((k_q4_wide<PL, SF32, GROUP, 4, 2, 2, 4>), grid, dim3(512), 0, st, c);
+        else hipLaunchKernelGGL((k_q4_wide<PL, SF32, GROUP, 2, 1, 1, 4>), grid, dim3(256), 0, st, c);
+    } else {
+        hipLaunchKernelGGL((k_q4_wide<PL, SF32, GROUP, 2, 1, 1, 4>), grid, dim3(256), 0, st, c);
+    }
+    if (p.S > 1) {
+        const int64_t n = (int64_t)a.N * a.M, jb = (n + 255) / 256;
+        hipLaunchKernelGGL(k_q4_join, dim3((unsigned)(jb < 65536 ? jb : 65536)), dim3(256), 0, st, a,
+                           (const float*)((char*)ws + p.part), p.S);
     }
 }
 
 template <int XT, bool SF32>
-void launch_q4(const Q4Args& a, int group, hipStream_t st) {
-    if (group == 32) launch_q4_group<XT, SF32, 32>(a, st);
-    else if (group == 64) launch_q4_group<XT, SF32, 64>(a, st);
-    else launch_q4_group<XT, SF32, 128>(a, st);
+void launch_q4(const Q4Args& a, int group, const Q4Plan& p, void* ws, hipStream_t st) {
+    if (group == 32) launch_q4_group<XT, SF32, 32>(a, p, ws, st);
+    else if (group == 64) launch_q4_group<XT, SF32, 64>(a, p, ws, st);
+    else launch_q4_group<XT, SF32, 128>(a, p, ws, st);
 }
 
 template <bool SIG>
@@ -539,7 +868,8 @@ extern "C" {
 
 int seedmm_q4_gemv(const uint32_t* weight, const void* scales, const void* biases, int s_dtype,
                    int group, const void* x, int x_dtype, int ldx, const float* x_scale, void* y,
-                   int y_dtype, int ldy, int M, int K, int N, void* hip_stream) {
+                   int y_dtype, int ldy, int M, int K, int N, void* workspace,
+                   size_t workspace_bytes, void* hip_stream) {
     if (group != 32 && group != 64 && group != 128) return SEEDMM_EINVAL;
     if (M < 0 || K < 0 || N < 0 || M > kMaxDim || K > kMaxDim || K % group != 0 || ldx < K || ldy < M) return SEEDMM_EINVAL;
     if (!float_type(s_dtype) || !float_type(y_dtype)) return SEEDMM_EINVAL;
@@ -563,12 +893,23 @@ int seedmm_q4_gemv(const uint32_t* weight, const void* scales, const void* biase
         return SEEDMM_EALIGN;
     const int per16 = x_dtype == SEEDMM_F32 ? 4 : x_dtype == SEEDMM_BF16 ? 8 : 16;
     if (N > 1 && ldx % per16 != 0) return SEEDMM_EALIGN;
+    const Q4Plan p = q4_plan(x_dtype, group, M, K, N);
+    if (p.wide && (!workspace || workspace_bytes < p.total)) return SEEDMM_EWORKSPACE;
+    if (p.wide && !aligned16(workspace)) return SEEDMM_EALIGN;
+    // one grid's workgroups are counted in 31 bits
+    if (p.wide && (int64_t)p.tn * p.tm > 0x7FFFFFFF) return SEEDMM_EINVAL;
     Q4Args a = {weight, scales, biases, x, x_scale, y, M, K, N, ldx, ldy, y_dtype == SEEDMM_BF16};
     const bool sf = s_dtype == SEEDMM_F32;
-    if (x_dtype == SEEDMM_F32) sf ? launch_q4<SEEDMM_F32, true>(a, group, st) : launch_q4<SEEDMM_F32, false>(a, group, st);
-    else if (x_dtype == SEEDMM_BF16) sf ? launch_q4<SEEDMM_BF16, true>(a, group, st) : launch_q4<SEEDMM_BF16, false>(a, group, st);
-    else sf ? launch_q4<SEEDMM_I8, true>(a, group, st) : launch_q4<SEEDMM_I8, false>(a, group, st);
+    if (x_dtype == SEEDMM_F32) sf ? launch_q4<SEEDMM_F32, true>(a, group, p, workspace, st) : launch_q4<SEEDMM_F32, false>(a, group, p, workspace, st);
+    else if (x_dtype == SEEDMM_BF16) sf ? launch_q4<SEEDMM_BF16, true>(a, group, p, workspace, st) : launch_q4<SEEDMM_BF16, false>(a, group, p, workspace, st);
+    else sf ? launch_q4<SEEDMM_I8, true>(a, group, p, workspace, st) : launch_q4<SEEDMM_I8, false>(a, group, p, workspace, st);
     return launch_status();
+}
+
+size_t seedmm_q4_workspace_bytes(int x_dtype, int group, int M, int K, int N) {
+    if (group != 32 && group != 64 && group != 128) return 0;
+    if (M < 0 || K < 0 || N < 0 || M > kMaxDim || K > kMaxDim || K % group != 0) return 0;
+    return q4_plan(x_dtype, group, M, K, N).total;
 }
 
 int seedmm_add_norm(const void* x, int x_dtype, int64_t ldx, const void* delta, int delta_dtype,
@@ -612,7 +953,7 @@ int seedmm_route(const void* logits, int l_dtype, int64_t ldl, const float* bias
 
 // Scratch of one block call: the normed rows, the logits, the routing (if the caller keeps
 // none) and the routed layer's own workspace.
-static bool block_layout(const seedmm_block* b, int T, size_t at[5]) {
+static bool block_layout(const seedmm_block* b, int T, size_t at[6]) {
     if (!b || T < 0 || b->E < 1 || b->H < 0) return false;
     const size_t layer = seedmm_moe_workspace_bytes(T, b->top_k, b->E, b->H, b->I);
     if (layer == 0) return false;
@@ -620,19 +961,20 @@ static bool block_layout(const seedmm_block* b, int T, size_t at[5]) {
     at[1] = at[0] + align_up((size_t)T * (size_t)b->E * 4);
     at[2] = at[1] + align_up((size_t)T * (size_t)b->top_k * 4);
     at[3] = at[2] + align_up((size_t)T * (size_t)b->top_k * 4);
-    at[4] = at[3] + layer;
+    at[4] = at[3] + align_up(seedmm_q4_workspace_bytes(SEEDMM_BF16, b->group, b->E, b->H, T));
+    at[5] = at[4] + layer;
     return true;
 }
 
 size_t seedmm_moe_block_workspace_bytes(const seedmm_block* block, int T) {
-    size_t at[5];
-    return block_layout(block, T, at) ? at[4] : 0;
+    size_t at[6];
+    return block_layout(block, T, at) ? at[5] : 0;
 }
 
 int seedmm_moe_block(const seedmm_block* block, void* r, int r_dtype, const void* delta,
                      int delta_dtype, float* y, int32_t* ids, float* w, int T, void* workspace,
                      size_t workspace_bytes, void* hip_stream, const seedmm_side* side) {
-    size_t at[5];
+    size_t at[6];
     if (!block || T < 0) return SEEDMM_EINVAL;
     const seedmm_block& b = *block;
     if (!block_layout(block, T, at)) return SEEDMM_EINVAL;
@@ -646,7 +988,7 @@ int seedmm_moe_block(const seedmm_block* block, void* r, int r_dtype, const void
         return e;
     if (int e = seedmm_q4_gemv(nullptr, nullptr, nullptr, b.router_dtype, b.group, nullptr,
                                SEEDMM_BF16, b.H, nullptr, nullptr, SEEDMM_F32, b.E, b.E, b.H, 0,
-                               hip_stream))
+                               nullptr, 0, hip_stream))
         return e;
     if (int e = seedmm_add_norm(nullptr, r_dtype, b.H, delta, delta_dtype, b.H, b.norm_weight,
                                 b.norm_dtype, b.eps, nullptr, b.H, nullptr, SEEDMM_BF16, b.H,
@@ -663,7 +1005,7 @@ int seedmm_moe_block(const seedmm_block* block, void* r, int r_dtype, const void
         !aligned16(b.router_weight) || !aligned16(b.router_scales) || !aligned16(b.router_biases) ||
         ((uintptr_t)b.router_bias & 3) || ((uintptr_t)ids & 3) || ((uintptr_t)w & 3))
         return SEEDMM_EALIGN;
-    if (!workspace || workspace_bytes < at[4]) return SEEDMM_EWORKSPACE;
+    if (!workspace || workspace_bytes < at[5]) return SEEDMM_EWORKSPACE;
     if (!aligned16(workspace)) return SEEDMM_EALIGN;
     char* ws = (char*)workspace;
     float* logits = (float*)(ws + at[0]);
@@ -675,13 +1017,13 @@ int seedmm_moe_block(const seedmm_block* block, void* r, int r_dtype, const void
     if (!e)
         e = seedmm_q4_gemv(b.router_weight, b.router_scales, b.router_biases, b.router_dtype, b.group,
                            ws, SEEDMM_BF16, b.H, nullptr, logits, SEEDMM_F32, b.E, b.E, b.H, T,
-                           hip_stream);
+                           ws + at[3], at[4] - at[3], hip_stream);
     if (!e)
         e = seedmm_route(logits, SEEDMM_F32, b.E, b.router_bias, b.score, T, b.E, b.top_k, ids, w,
                          hip_stream);
     if (!e)
         e = seedmm_moe_ex(ids, w, T, b.top_k, ws, y, b.E, b.H, b.I, b.P, b.p4mask, b.gate, b.up,
-                          b.down, ws + at[3], at[4] - at[3], hip_stream, side);
+                          b.down, ws + at[4], at[5] - at[4], hip_stream, side);
     return e;
 }
 

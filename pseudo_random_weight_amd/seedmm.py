@@ -85,7 +85,10 @@ def _load():
     L.seedmm_cache_moe.argtypes = [p, p, p, p, i32, i32, p, p, p, sz, p]
     L.seedmm_cache_stats.argtypes = [p, p]
     i64 = ctypes.c_int64
-    L.seedmm_q4_gemv.argtypes = [p, p, p, i32, i32, p, i32, i32, p, p, i32, i32, i32, i32, i32, p]
+    L.seedmm_q4_gemv.argtypes = [p, p, p, i32, i32, p, i32, i32, p, p, i32, i32, i32, i32, i32, p,
+                                 sz, p]
+    L.seedmm_q4_workspace_bytes.restype = sz
+    L.seedmm_q4_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
     L.seedmm_add_norm.argtypes = [p, i32, i64, p, i32, i64, p, i32, ctypes.c_float, p, i64, p, i32,
                                   i64, p, i32, i32, p]
     L.seedmm_route.argtypes = [p, i32, i64, p, i32, i32, i32, i32, p, p, p]
@@ -117,7 +120,8 @@ EXPORTS = ("seedmm_gemv", "seedmm_gemv_ex", "seedmm_reconstruct", "seedmm_moe_di
            "seedmm_search_prepare", "seedmm_cache_record_layout", "seedmm_cache_state_bytes",
            "seedmm_cache_device_bytes",
            "seedmm_cache_init", "seedmm_cache_reset", "seedmm_cache_plan", "seedmm_cache_moe",
-           "seedmm_cache_stats", "seedmm_q4_gemv", "seedmm_add_norm", "seedmm_route",
+           "seedmm_cache_stats", "seedmm_q4_gemv", "seedmm_q4_workspace_bytes",
+           "seedmm_add_norm", "seedmm_route",
            "seedmm_moe_block_workspace_bytes", "seedmm_moe_block", "seedmm_strerror",
            "seedmm_version")
 
@@ -681,11 +685,17 @@ def _check_q4(mat, M, K, group, dev):
     return sd
 
 
+def q4_workspace_bytes(x_dtype, group: int, M: int, K: int, N: int) -> int:
+    """Bytes of the workspace that q4_gemv needs for N rows of x_dtype."""
+    return int(_lib.seedmm_q4_workspace_bytes(_ROWS[x_dtype], group, M, K, N))
+
+
 def q4_gemv(mat: dict, x: torch.Tensor, M: int, K: int, group: int = 64, x_scale=None, y=None,
-            y_dtype=torch.float32, stream=None):
+            y_dtype=torch.float32, workspace=None, stream=None):
     """y = x W^T for W in affine 4 bits (seedmm_q4_gemv).  mat: {"weight": uint32 [M*K/8],
     "scales", "biases": fp32 or bf16 [M*K/group]}; x fp32, bf16 or int8 [N][K] (or [K]),
-    int8 rows with x_scale fp32 [N]; y [N][M] (or [M]) fp32 or bf16."""
+    int8 rows with x_scale fp32 [N]; y [N][M] (or [M]) fp32 or bf16.  workspace: a GPU tensor
+    of q4_workspace_bytes(...) bytes, allocated here if it is needed and not given."""
     xd, N, cols, ldx = _row_tensor(x, _ROWS, "x")
     dev = x.get_device()
     if cols < K:
@@ -701,9 +711,20 @@ def q4_gemv(mat: dict, x: torch.Tensor, M: int, K: int, group: int = 64, x_scale
     yd, yn, yc, ldy = _row_tensor(y, _FLOATS, "y", dev)
     if yn < N or yc < M:
         raise ValueError(f"y must hold [{N}][{M}]")
+    ws = nws = None
+    if workspace is None and N > 5:
+        need = q4_workspace_bytes(x.dtype, group, M, K, N)
+        if need:
+            with _on(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("the workspace must be a contiguous tensor on x's device")
+        ws, nws = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _launch(dev, stream, "seedmm_q4_gemv", _lib.seedmm_q4_gemv, mat["weight"].data_ptr(),
             mat["scales"].data_ptr(), mat["biases"].data_ptr(), sd, group, x.data_ptr(), xd, ldx,
-            None if x_scale is None else x_scale.data_ptr(), y.data_ptr(), yd, ldy, M, K, N)
+            None if x_scale is None else x_scale.data_ptr(), y.data_ptr(), yd, ldy, M, K, N,
+            ws, nws or 0)
     return y
 
 

@@ -112,7 +112,7 @@ def test_q4_gemv(sm, x, group, N, M, K):
 
 @pytest.mark.parametrize("x", ["bf16", "i8", "f32"])
 @pytest.mark.parametrize("s,y", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16")])
-@pytest.mark.parametrize("N,M,K,group", [(1, 50, 96, 32), (3, 21, 192, 64), (40, 90, 1088, 64),
+@pytest.mark.parametrize("N,M,K,group", [(1, 50, 96, 32), (3, 21, 192, 64), (40, 90, 1088, 64), (20, 40, 32, 32),
                                          (200, 150, 160, 32), (1, 130, 4160, 64), (9, 300, 8320, 128)])
 def test_q4_gemv_types(sm, x, s, y, N, M, K, group):
     check_q4(sm, N, M, K, group, x, s, y, 2)
