@@ -314,6 +314,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_q4(const Q4Args a, int slab) {
 // A wave holds MT tiles of 32 weight rows by TT tiles of 32 tokens.  Lane r + 32 h loads the
 // 16 bytes of row r that hold columns 32 h .. 32 h + 31 of a 64-column step: word j is its
 // operand of instruction j with no exchange (groups of 32: after one swap of the halves).
+constexpr int kQ4Band = 512;
 struct Q4Wide {
     Q4Args a;
     const uint16_t* xp;   // [PL][N][Kp] rows in the operands' order, zero past K
@@ -382,64 +383,78 @@ __global__ __launch_bounds__(256) void k_q4_rows(const Q4Args a, uint16_t* xp, u
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-template <int PL, bool SF32, int GROUP, int TT, int MT, int WN, int WM>
-__global__ __launch_bounds__(WN * WM * 64) void k_q4_wide(const Q4Wide c) {
+template <int PL, bool SF32, int GROUP, int TT, int MT, int WN, int WM, int SP, int OCC>
+__global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OCC))) void k_q4_wide(const Q4Wide c) {
     constexpr int BT = 32 * TT * WN, BM = 32 * MT * WM, NTH = 64 * WN * WM;
     constexpr int NST = PL * BT * 8 / NTH;      // 16-byte pieces of a step a thread stages
-    static_assert(PL * BT * 8 % NTH == 0, "whole pieces");
-    __shared__ u32x4 xs[2][PL * BT * 8];
+    constexpr int CW = 2 * SP;                  // 16-byte pieces of a weight row in a slab
+    constexpr int NWT = BM * CW / NTH;
+    static_assert(PL * BT * 8 % NTH == 0 && BM * CW % NTH == 0, "whole pieces");
+    __shared__ u32x4 xs[SP][PL * BT * 8];
+    __shared__ u32x4 ws[BM * CW];
     const Q4Args& a = c.a;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wn = wave / WM, wm = wave % WM;
     const int r = lane & 31, h = lane >> 5;
-    // workgroups of one XCD (every eighth) take neighbouring tiles, token tiles first
+    // workgroups of one XCD (every eighth) take neighbouring tiles: columns of kQ4Band tokens
+    // by all weight rows, so that its L2 holds the activations of a column
     const int total = c.tn * c.tm;
     int id = blockIdx.x;
     if (total % 8 == 0) id = (id & 7) * (total >> 3) + (id >> 3);
-    const int n0 = (id % c.tn) * BT;
-    const int64_t m0 = (int64_t)(id / c.tn) * BM + 32 * MT * wm;
+    constexpr int GT = kQ4Band / BT;
+    const int col = id / (GT * c.tm), in = id - col * GT * c.tm;
+    const int width = min(GT, c.tn - col * GT);
+    const int n0 = (col * GT + in % width) * BT;
+    const int64_t mb = (int64_t)(in / width) * BM, m0 = mb + 32 * MT * wm;
     const int kb = blockIdx.y * c.ksplit, ke = min(a.K, kb + c.ksplit);
     const int G = a.K / GROUP;
 
-    // staging: piece u = 16 bytes `u & 7` of tile row u >> 3, kept at slot (u & 7) ^ (row & 7)
-    int64_t src[NST];
-    int dst[NST];
+    // Slabs of SP steps (64 columns each).  Piece u of a step = 16 bytes `u & 7` of tile row
+    // u >> 3, kept at slot (u & 7) ^ (row & 7); the codes likewise, CW pieces a row.
+    int64_t src[NST], wsrc[NWT];
+    int dst[NST], wdst[NWT];
 #pragma unroll
     for (int i = 0; i < NST; ++i) {
         const int u = i * NTH + tid, row = u >> 3, p = row / BT, t = row % BT;
         src[i] = ((int64_t)p * a.N + min(n0 + t, a.N - 1)) * c.Kp + 8 * (u & 7);
         dst[i] = row * 8 + ((u & 7) ^ (row & 7));
     }
-    u32x4 stage[NST];
+#pragma unroll
+    for (int i = 0; i < NWT; ++i) {
+        const int u = i * NTH + tid, row = u / CW;
+        wsrc[i] = (mb + row < a.M ? mb + row : a.M - 1) * (a.K / 8);
+        wdst[i] = row * CW + ((u % CW) ^ (row & (CW - 1)));
+    }
+    int64_t row[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) row[mt] = m0 + 32 * mt + r < a.M ? m0 + 32 * mt + r : a.M - 1;
+    constexpr int NG = GROUP == 32 ? 2 : 1;               // groups a step
+    constexpr int NGS = 64 * SP >= GROUP ? 64 * SP / GROUP : 1;
+    u32x4 stage[SP][NST], wstage[NWT];
+    Scales<SF32, NGS> snext[MT];
+    // Rows of activations are zero from K to Kp.  Past K the codes of the row's last columns
+    // are loaded again, and scales are 0.
     auto fetch = [&](int k) {
 #pragma unroll
-        for (int i = 0; i < NST; ++i) stage[i] = *(const u32x4*)(c.xp + src[i] + k);
-    };
-    auto put = [&](int buf) {
+        for (int b = 0; b < SP; ++b)
 #pragma unroll
-        for (int i = 0; i < NST; ++i) xs[buf][dst[i]] = stage[i];
-    };
-    int64_t row[MT];
-    const uint32_t* wrow[MT];
+            for (int i = 0; i < NST; ++i) stage[b][i] = *(const u32x4*)(c.xp + src[i] + k + 64 * b);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        row[mt] = m0 + 32 * mt + r < a.M ? m0 + 32 * mt + r : a.M - 1;
-        wrow[mt] = a.w + row[mt] * (a.K / 8) + 4 * h;
-    }
-    constexpr int NG = GROUP == 32 ? 2 : 1;      // groups a step
-    u32x4 wv[MT];
-    float sv[MT][NG];
-    auto weights = [&](int k) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            wv[mt] = u32x4{0u, 0u, 0u, 0u};
-            if (k + 32 * h < a.K) wv[mt] = *(const u32x4*)(wrow[mt] + k / 8);
-            Scales<SF32, NG> s;
-            s.load(a.s, row[mt] * G + k / GROUP, G - k / GROUP);
-#pragma unroll
-            for (int g = 0; g < NG; ++g) sv[mt][g] = s.get(g);
+        for (int i = 0; i < NWT; ++i) {
+            const int kw = k + 32 * ((i * NTH + tid) % CW);
+            wstage[i] = *(const u32x4*)(a.w + wsrc[i] + (kw < a.K ? kw : a.K - 32) / 8);
         }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) snext[mt].load(a.s, row[mt] * G + k / GROUP, G - k / GROUP);
+    };
+    auto put = [&]() {
+#pragma unroll
+        for (int b = 0; b < SP; ++b)
+#pragma unroll
+            for (int i = 0; i < NST; ++i) xs[b][dst[i]] = stage[b][i];
+#pragma unroll
+        for (int i = 0; i < NWT; ++i) ws[wdst[i]] = wstage[i];
     };
 
     f32x16 acc[TT][MT];
@@ -450,9 +465,8 @@ __global__ __launch_bounds__(WN * WM * 64) void k_q4_wide(const Q4Wide c) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[tt][mt][i] = 0.f;
     fetch(kb);
-    weights(kb);
-    if (blockIdx.y == 0) {      // bias term
-        for (int g0 = 0; g0 < G; g0 += 16) {
+    {   // bias term: the splits take 16 groups in turn
+        for (int g0 = 16 * blockIdx.y; g0 < G; g0 += 16 * gridDim.y) {
             const int gl = g0 + 8 * h;
             bf16x8 bb[MT][SF32 ? 3 : 1];
 #pragma unroll
@@ -491,61 +505,116 @@ __global__ __launch_bounds__(WN * WM * 64) void k_q4_wide(const Q4Wide c) {
             }
         }
     }
-    put(0);
+    put();
     __syncthreads();
 
-    int buf = 0;
-    for (int k = kb; k < ke; k += 64, buf ^= 1) {
-        const bool more = k + 64 < ke;
-        bf16x8 bq[MT][4];
+    // Tile i's chain of instructions runs while the vector units add tile i - 1 (the last
+    // tile's addition is carried into the next step) and unpack the next codes.
+    constexpr int NT = TT * MT, JC = 4 / NG;   // tiles; instructions a group
+    static_assert(NT == 1 || NT % 2 == 0, "the carried tile's sums are not the first's");
+    f32x16 d[2][NG];
+    float sp[NG];                              // the carried tile's scales
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        sp[g] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) d[NT == 1 ? 1 : (NT - 1) & 1][g][i] = 0.f;
+    }
+    // A slab's activations, codes and scales are loaded while the one before is multiplied
+    // and take its place in LDS after it.
+    Scales<SF32, NGS> sc[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) sc[mt] = snext[mt];
+    auto step = [&](int b) {
+        uint32_t w[MT][4];
         float s[MT][NG];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            uint32_t w[4] = {wv[mt][0], wv[mt][1], wv[mt][2], wv[mt][3]};
-            if constexpr (GROUP == 32) {
-                auto x = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-                auto y = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-                w[0] = x[0]; w[2] = x[1]; w[1] = y[0]; w[3] = y[1];
+            const int wr = 32 * (MT * wm + mt) + r;
+            const u32x4 wv = ws[wr * CW + ((2 * b + h) ^ (wr & (CW - 1)))];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[mt][j] = wv[j];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) s[mt][g] = sc[mt].get(64 * b / GROUP + g);
+        }
+        bf16x8 bq[MT][4], xa[PL][4];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int tt = i / MT, mt = i % MT;
+            if (mt == 0) {
+                const int t = 32 * (TT * wn + tt) + r;
+#pragma unroll
+                for (int p = 0; p < PL; ++p)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int ch = GROUP == 32 ? 4 * (j >> 1) + 2 * h + (j & 1) : 4 * h + j;
+                        xa[p][j] = __builtin_bit_cast(bf16x8, xs[b][(p * BT + t) * 8 + (ch ^ (t & 7))]);
+                    }
+            }
+            if (tt == 0) {
+                if constexpr (GROUP == 32) {
+                    auto x = __builtin_amdgcn_permlane32_swap(w[mt][0], w[mt][2], false, false);
+                    auto y = __builtin_amdgcn_permlane32_swap(w[mt][1], w[mt][3], false, false);
+                    w[mt][0] = x[0]; w[mt][2] = x[1]; w[mt][1] = y[0]; w[mt][3] = y[1];
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) bq[mt][j] = codes_bf16(w[mt][j]);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) bq[mt][j] = codes_bf16(w[j]);
+            for (int g = 0; g < NG; ++g) {
+                f32x16 e = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int g = 0; g < NG; ++g) s[mt][g] = sv[mt][g];
+                for (int p = 0; p < PL; ++p)
+#pragma unroll
+                    for (int j = g * JC; j < (g + 1) * JC; ++j)
+                        e = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[p][j], bq[mt][j], e, 0, 0, 0);
+                d[i & 1][g] = e;
+            }
+            const int q = (i + NT - 1) % NT, qt = q / MT, qm = q % MT;   // the tile before
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const float sq = i == 0 ? sp[g] : s[qm][g];
+#pragma unroll
+                for (int v = 0; v < 16; ++v)
+                    acc[qt][qm][v] = __builtin_fmaf(sq, d[NT == 1 ? 1 : q & 1][g][v], acc[qt][qm][v]);
+            }
+            if constexpr (NT == 1) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g) d[1][g] = d[0][g];
+            }
         }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) sp[g] = s[MT - 1][g];
+        // spread the vector work between the instructions of a step (4096 x 8192 x 2048:
+        // 200 -> 185 us; one tile a wave gains nothing by it)
+        if constexpr (TT == 2 && PL == 1) {
+#pragma unroll
+            for (int i = 0; i < 4 * NT; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
+            }
+        }
+    };
+    for (int k = kb; k < ke; k += 64 * SP) {
+        const bool more = k + 64 * SP < ke;
+        if (more) fetch(k + 64 * SP);
+#pragma unroll
+        for (int b = 0; b < SP; ++b)
+            if (k + 64 * b < ke) step(b);
         if (more) {
-            fetch(k + 64);
-            weights(k + 64);
+            __syncthreads();
+            put();
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) sc[mt] = snext[mt];
+            __syncthreads();
         }
-#pragma unroll
-        for (int tt = 0; tt < TT; ++tt) {
-            const int t = 32 * (TT * wn + tt) + r;
-            bf16x8 xa[PL][4];
-#pragma unroll
-            for (int p = 0; p < PL; ++p)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int ch = GROUP == 32 ? 4 * (j >> 1) + 2 * h + (j & 1) : 4 * h + j;
-                    xa[p][j] = __builtin_bit_cast(bf16x8, xs[buf][(p * BT + t) * 8 + (ch ^ (t & 7))]);
-                }
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    f32x16 d = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int p = 0; p < PL; ++p)
-#pragma unroll
-                        for (int j = g * 4 / NG; j < (g + 1) * 4 / NG; ++j)
-                            d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[p][j], bq[mt][j], d, 0, 0, 0);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        acc[tt][mt][i] = __builtin_fmaf(s[mt][g], d[i], acc[tt][mt][i]);
-                }
-            }
-        }
-        if (more) put(buf ^ 1);
-        __syncthreads();
     }
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+            acc[TT - 1][MT - 1][v] =
+                __builtin_fmaf(sp[g], d[NT == 1 ? 1 : (NT - 1) & 1][g][v], acc[TT - 1][MT - 1][v]);
 
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt)
@@ -782,7 +851,8 @@ void launch_q4_jn(const Q4Args& a, hipStream_t st) {
 // The plan of a product with many tokens: what its workspace holds.
 struct Q4Plan {
     bool wide;
-    int Kp, Gp, S, ksplit, cfg, tn, tm;
+    bool two;                      // tiles of 64 tokens, else of 32
+    int Kp, Gp, S, ksplit, tn, tm;
     size_t xg, part, total;
 };
 
@@ -791,22 +861,24 @@ Q4Plan q4_plan(int x_dtype, int group, int M, int K, int N) {
     const int PL = x_dtype == SEEDMM_F32 ? 3 : 1;
     p.wide = (int64_t)N * PL > 16 && M > 0 && K > 0;
     if (!p.wide) return p;
-    p.Kp = (K + 63) / 64 * 64;
+    p.Kp = (K + 255) / 256 * 256;
     p.Gp = (K / group + 15) / 16 * 16;
-    // tiles: 256 x 256 where they fill the chip, else 64 x 128 with K split until they do
-    const int64_t big = ((int64_t)(N + 255) / 256) * ((M + 255) / 256);
-    p.cfg = PL == 1 && big >= 256 ? 1 : 0;
-    const int BT = p.cfg ? 256 : 64, BM = p.cfg ? 256 : 128;
+    // Tiles of 64 tokens by 128 weight rows where they make 512 workgroups (two a CU);
+    // else of 32 by 128 with K split until they do (256 x 8192 x 2048: 26 us against 31;
+    // 61 x 5125 x 4160: one split 73 us, seven 24 us).  fp32 rows are three planes of work:
+    // always 64.
+    const int64_t tm = ((int64_t)M + 127) / 128;
+    p.two = PL == 3 || (((int64_t)N + 63) / 64) * tm >= 512;
+    const int BT = p.two ? 64 : 32, slab = PL == 3 ? 128 : 256;
     p.tn = (int)(((int64_t)N + BT - 1) / BT);
-    p.tm = (int)(((int64_t)M + BM - 1) / BM);
-    const int steps = (K + 127) / 128;
-    int64_t S = p.cfg ? 1 : 512 / ((int64_t)p.tn * p.tm);
-    if (S > steps / 2) S = steps / 2;
+    p.tm = (int)tm;
+    const int slabs = (K + slab - 1) / slab;
+    int64_t S = (511 + p.tn * tm) / (p.tn * tm);
+    if (S > slabs) S = slabs;
     if (S > 16) S = 16;
-    if (S < 1) S = 1;
-    const int per = (int)((steps + S - 1) / S);
-    p.ksplit = per * 128;
-    p.S = (steps + per - 1) / per;
+    const int per = (int)((slabs + S - 1) / S);
+    p.ksplit = per * slab;
+    p.S = (slabs + per - 1) / per;
     p.xg = align_up((size_t)PL * (size_t)N * (size_t)p.Kp * 2);
     p.part = p.xg + align_up((size_t)3 * (size_t)N * (size_t)p.Gp * 2);
     p.total = p.part + (p.S > 1 ? align_up((size_t)p.S * (size_t)N * (size_t)M * 4) : 0);
@@ -828,12 +900,9 @@ void launch_q4_group(const Q4Args& a, const Q4Plan& p, void* ws, hipStream_t st)
                        dim3(256), 0, st, a, xp, xg, p.Kp, p.Gp);
     Q4Wide c = {a, xp, xg, p.S > 1 ? (float*)((char*)ws + p.part) : nullptr, p.Kp, p.Gp, p.ksplit, p.tn, p.tm};
     const dim3 grid((unsigned)((int64_t)p.tn * p.tm), (unsigned)p.S);
-    if constexpr (PL == 1) {
-        if (p.cfg) hipLaunchKernelGGL((k_q4_wide<PL, SF32, GROUP, 4, 2, 2, 4>), grid, dim3(512), 0, st, c);
-        else hipLaunchKernelGGL((k_q4_wide<PL, SF32, GROUP, 2, 1, 1, 4>), grid, dim3(256), 0, st, c);
-    } else {
-        hipLaunchKernelGGL((k_q4_wide<PL, SF32, GROUP, 2, 1, 1, 4>), grid, dim3(256), 0, st, c);
-    }
+    if constexpr (PL == 3) hipLaunchKernelGGL((k_q4_wide<PL, SF32, GROUP, 2, 1, 1, 4, 2, 2>), grid, dim3(256), 0, st, c);
+    else if (p.two) hipLaunchKernelGGL((k_q4_wide<PL, SF32, GROUP, 2, 1, 1, 4, 4, 2>), grid, dim3(256), 0, st, c);
+    else hipLaunchKernelGGL((k_q4_wide<PL, SF32, GROUP, 1, 1, 1, 4, 4, 3>), grid, dim3(256), 0, st, c);
     if (p.S > 1) {
         const int64_t n = (int64_t)a.N * a.M, jb = (n + 255) / 256;
         hipLaunchKernelGGL(k_q4_join, dim3((unsigned)(jb < 65536 ? jb : 65536)), dim3(256), 0, st, a,
