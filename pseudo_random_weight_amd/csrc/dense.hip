@@ -59,6 +59,14 @@ __device__ __forceinline__ void transpose_quarters(uint32_t (&w)[4]) {
     w[0] = c[0]; w[1] = c[1]; w[2] = d[0]; w[3] = d[1];
 }
 
+// LDS accesses of one wave keep their order across this point (they run in order; the
+// compiler must not exchange them).
+__device__ __forceinline__ void wave_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // 8 codes -> bf16 in the order 0 2 4 6 1 3 5 7.  A byte 0 .. 15 read as an 8-bit float
 // (e4m3) is code * 2^-9 exactly, subnormal or not, so the pair conversion with scale 2^9
 // gives the integers: 7 instructions for 8 codes.
@@ -105,14 +113,33 @@ struct Scales {
     }
 };
 
-// Stages 8 columns of activation row `src` (or zeros) in the operands' order: XT rows `dst`
-// apart by `rowb` (fp32: three).  Returns the columns' sum.
+// 8 columns of an activation row: load8 takes them from memory (or zeros), place8 writes
+// them to LDS in the operands' order, XT rows `rowb` apart (fp32: three), and returns
+// their sum.
 template <int XT>
-__device__ __forceinline__ float stage8(const void* x, int64_t at, bool ok, char* dst, int64_t rowb) {
+struct Raw8 {
+    uint32_t u[XT == SEEDMM_F32 ? 8 : XT == SEEDMM_BF16 ? 4 : 2];
+};
+
+template <int XT>
+__device__ __forceinline__ Raw8<XT> load8(const void* x, int64_t at, bool ok) {
+    Raw8<XT> v = {};
+    if (ok) {
+        if constexpr (XT == SEEDMM_I8) *(u32x2*)v.u = *(const u32x2*)((const int8_t*)x + at);
+        else if constexpr (XT == SEEDMM_BF16) *(u32x4*)v.u = *(const u32x4*)((const uint16_t*)x + at);
+        else {
+            *(u32x4*)v.u = *(const u32x4*)((const float*)x + at);
+            *(u32x4*)(v.u + 4) = *(const u32x4*)((const float*)x + at + 4);
+        }
+    }
+    return v;
+}
+
+template <int XT>
+__device__ __forceinline__ float place8(const Raw8<XT>& x, char* dst, int64_t rowb) {
+    const uint32_t* v = x.u;
     float sum = 0.f;
     if constexpr (XT == SEEDMM_I8) {
-        u32x2 v = {0u, 0u};
-        if (ok) v = *(const u32x2*)((const int8_t*)x + at);
         int isum = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) isum += (int)(int8_t)(v[0] >> 8 * i) + (int)(int8_t)(v[1] >> 8 * i);
@@ -122,8 +149,6 @@ __device__ __forceinline__ float stage8(const void* x, int64_t at, bool ok, char
         p[1] = __builtin_amdgcn_perm(v[1], v[0], 0x07050301u);
         *(u32x2*)dst = p;
     } else if constexpr (XT == SEEDMM_BF16) {
-        u32x4 v = {0u, 0u, 0u, 0u};
-        if (ok) v = *(const u32x4*)((const uint16_t*)x + at);
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum += __uint_as_float(v[i] << 16) + __uint_as_float(v[i] & 0xFFFF0000u);
         u32x4 p;
@@ -133,15 +158,10 @@ __device__ __forceinline__ float stage8(const void* x, int64_t at, bool ok, char
         p[3] = __builtin_amdgcn_perm(v[3], v[2], 0x07060302u);   // x5 x7
         *(u32x4*)dst = p;
     } else {
-        f32x4 v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        if (ok) {
-            v[0] = *(const f32x4*)((const float*)x + at);
-            v[1] = *(const f32x4*)((const float*)x + at + 4);
-        }
         uint32_t pl[3][8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float f = v[i >> 2][i & 3];
+            float f = __uint_as_float(v[i]);
             sum += f;
 #pragma unroll
             for (int p = 0; p < 3; ++p) {
@@ -164,19 +184,23 @@ __device__ __forceinline__ float stage8(const void* x, int64_t at, bool ok, char
 }
 
 // A few tokens.  A wave takes 16 weight rows; KW waves of a workgroup share a row tile and
-// take its 128-column steps in turn, PF steps loaded ahead of the ones multiplied, the first
-// before the activations are staged.  The D tile of 16x16x32 instructions has a row a
-// token: up to 4 activation rows sit in D rows 0, 4, 8, 12 (JN = 1), so each lane scales
-// one value a group instead of four.
-template <int XT, bool SF32, int GROUP, int JN, int WAVES, int KW>
+// take its slabs of SS * 128 columns in turn, each loaded while the one before is
+// multiplied, the first before the activations are staged.
+//   SS = 1: each lane loads the 16 bytes that it multiplies (a row's 64 bytes by 4 lanes).
+//   SS = 4: 16 lanes load 256 bytes of a row, whole cache lines, and the wave's own piece
+//     of LDS hands them to the lanes that multiply them.
+// The D tile of 16x16x32 instructions has a row a token: up to 4 activation rows sit in D
+// rows 0, 4, 8, 12 (JN = 1), so each lane scales one value a group instead of four.
+template <int XT, bool SF32, int GROUP, int JN, int WAVES, int KW, int SS>
 __global__ __launch_bounds__(WAVES * 64) void k_q4(const Q4Args a, int slab) {
     constexpr int PL = XT == SEEDMM_F32 ? 3 : 1;       // operand rows a token
     constexpr int EB = XT == SEEDMM_I8 ? 1 : 2;
-    constexpr int NG = 128 / GROUP;
-    constexpr int PF = KW >= 16 ? 1 : 4;
+    constexpr int NG = 128 / GROUP;                    // groups of 128 columns
     constexpr int RW = WAVES / KW;
     constexpr int SXW = JN == 1 ? 4 : 16;
+    constexpr int SC = SS * 128;                       // columns of a wave's slab
     __shared__ float red[KW][RW][JN * 4][17];
+    __shared__ u32x4 bounce[SS == 4 ? WAVES : 1][SS == 4 ? 256 : 1];
     extern __shared__ __align__(16) char lds[];
     const int rowb = slab * EB + 16;
     float* sx = (float*)lds;                                     // [slab / GROUP][SXW]
@@ -189,45 +213,59 @@ __global__ __launch_bounds__(WAVES * 64) void k_q4(const Q4Args a, int slab) {
     const int64_t m0 = ((int64_t)blockIdx.x * RW + rw) * 16;
     const int64_t row = m0 + r < a.M ? m0 + r : a.M - 1;
     const int G = a.K / GROUP;
-    const uint32_t* wrow = a.w + row * (a.K / 8) + 4 * q;
+    // this lane's piece of load i: row lrow[i], columns 32 lcol ..
+    const int lcol = SS == 4 ? r : q;
+    const uint32_t* lrow[SS];
+#pragma unroll
+    for (int i = 0; i < SS; ++i) {
+        const int64_t m = SS == 4 ? m0 + 4 * i + q : m0 + r;
+        lrow[i] = a.w + (m < a.M ? m : a.M - 1) * (a.K / 8);
+    }
     const int xrow = JN == 1 ? min(r >> 2, rows - 1) : min(r, rows - 1);
     const char* xl = xs + xrow * rowb + (XT == SEEDMM_I8 ? 8 : 16) * q;
 
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     for (int k0 = 0; k0 < a.K; k0 += slab) {
         const int kn = min(slab, a.K - k0);
-        const int ns = (kn + 127) / 128;
-        u32x4 w[2][PF];
-        Scales<SF32, NG> ss[2][PF], bs[2][PF];
-        auto load = [&](int buf, int it) {
+        u32x4 w[SS];
+        Scales<SF32, NG * SS> ss, bs;
+        // past K the last columns' codes are loaded again: they meet activations of zero
+        auto load = [&](int c0) {
+            const int k = k0 + c0 + 32 * lcol;
 #pragma unroll
-            for (int p = 0; p < PF; ++p) {
-                const int st = (it + p) * KW + kw;
-                if (st < ns) {
-                    w[buf][p] = u32x4{0u, 0u, 0u, 0u};
-                    if (st * 128 + 32 * q < kn) w[buf][p] = *(const u32x4*)(wrow + (k0 + st * 128) / 8);
-                    const int g = k0 / GROUP + st * NG;
-                    ss[buf][p].load(a.s, row * G + g, G - g);
-                    bs[buf][p].load(a.b, row * G + g, G - g);
-                }
-            }
+            for (int i = 0; i < SS; ++i) w[i] = *(const u32x4*)(lrow[i] + (k < a.K ? k : a.K - 32) / 8);
+            const int g = (k0 + c0) / GROUP;
+            ss.load(a.s, row * G + g, G - g);
+            bs.load(a.b, row * G + g, G - g);
         };
-        load(0, 0);
+        if (kw * SC < kn) load(kw * SC);
         if (k0) __syncthreads();
-        const int per_row = slab / 8;
-        for (int u = tid; u < a.N * per_row; u += WAVES * 64) {
-            const int t = u / per_row, kk = (u - t * per_row) * 8;
-            float sum = stage8<XT>(a.x, (int64_t)t * a.ldx + k0 + kk, kk < kn,
-                                   xs + t * PL * rowb + kk * EB, rowb);
+        const int per_row = slab / 8, units = a.N * per_row;
+        for (int u0 = tid; u0 < units; u0 += WAVES * 64 * 4) {   // whole waves: units % 64 == 0 or one batch
+            Raw8<XT> raw[4];
 #pragma unroll
-            for (int d = 1; d < GROUP / 8; d *= 2) sum += __shfl_xor(sum, d);
-            if (kk % GROUP == 0) {
+            for (int i = 0; i < 4; ++i) {
+                const int u = u0 + i * WAVES * 64, t = u / per_row, kk = (u - t * per_row) * 8;
+                raw[i] = load8<XT>(a.x, (int64_t)t * a.ldx + k0 + kk, u < units && kk < kn);
+            }
 #pragma unroll
-                for (int p = 0; p < PL; ++p) sx[kk / GROUP * SXW + t * PL + p] = p ? 0.f : sum;
+            for (int i = 0; i < 4; ++i) {
+                const int u = u0 + i * WAVES * 64, t = u / per_row, kk = (u - t * per_row) * 8;
+                if (u < units) {
+                    float sum = place8<XT>(raw[i], xs + t * PL * rowb + kk * EB, rowb);
+#pragma unroll
+                    for (int d = 1; d < GROUP / 8; d *= 2) sum += __shfl_xor(sum, d);
+                    if (kk % GROUP == 0) {
+#pragma unroll
+                        for (int p = 0; p < PL; ++p) sx[kk / GROUP * SXW + t * PL + p] = p ? 0.f : sum;
+                    }
+                }
             }
         }
         __syncthreads();
-        auto step = [&](const u32x4& wv, const Scales<SF32, NG>& sv, const Scales<SF32, NG>& bv, int st) {
+        // 128 columns from column 128 st of the staged ones: the wave's codes, and its scales
+        // from group 128 j / GROUP of the slab's
+        auto step = [&](const u32x4& wv, const Scales<SF32, NG * SS>& sv, const Scales<SF32, NG * SS>& bv, int st, int j0) {
             uint32_t c[4] = {wv[0], wv[1], wv[2], wv[3]};
             transpose_quarters(c);
             const char* xp = xl + st * 128 * EB;
@@ -257,7 +295,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_q4(const Q4Args a, int slab) {
                     for (int j = g * (GROUP / 32); j < (g + 1) * (GROUP / 32); ++j)
                         d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(*(const bf16x8*)(xp + 64 * j), codes_bf16(c[j]), d, 0, 0, 0);
                 }
-                const float s = sv.get(g), b = bv.get(g);
+                const float s = sv.get(j0 * NG + g), b = bv.get(j0 * NG + g);
                 if constexpr (JN == 1) {
                     acc[0] = __builtin_fmaf(s, d[0], __builtin_fmaf(b, sx[gl * 4 + q], acc[0]));
                 } else {
@@ -268,16 +306,24 @@ __global__ __launch_bounds__(WAVES * 64) void k_q4(const Q4Args a, int slab) {
                 }
             }
         };
-        const int nit = (ns - kw + KW - 1) / KW;      // this wave's steps
-        for (int it = 0; it < nit; it += 2 * PF) {
-            load(1, it + PF);
+        for (int c0 = kw * SC; c0 < kn; c0 += KW * SC) {
+            const Scales<SF32, NG * SS> sc = ss, bc = bs;
+            u32x4 v[SS];
+            if constexpr (SS == 4) {
+                u32x4* const bw = bounce[wave];
 #pragma unroll
-            for (int p = 0; p < PF; ++p)
-                if (it + p < nit) step(w[0][p], ss[0][p], bs[0][p], (it + p) * KW + kw);
-            load(0, it + 2 * PF);
+                for (int i = 0; i < 4; ++i) bw[(4 * i + q) * 16 + (r ^ (4 * i + q))] = w[i];
+                wave_order();
 #pragma unroll
-            for (int p = 0; p < PF; ++p)
-                if (it + PF + p < nit) step(w[1][p], ss[1][p], bs[1][p], (it + PF + p) * KW + kw);
+                for (int j = 0; j < 4; ++j) v[j] = bw[r * 16 + ((4 * j + q) ^ r)];
+                wave_order();
+            } else {
+                v[0] = w[0];
+            }
+            if (c0 + KW * SC < kn) load(c0 + KW * SC);
+#pragma unroll
+            for (int j = 0; j < SS; ++j)
+                if (c0 + 128 * j < kn) step(v[j], sc, bc, c0 / 128 + j, j);
         }
     }
     // the KW partial tiles meet in LDS in their order; D column = weight row
@@ -361,7 +407,7 @@ __global__ __launch_bounds__(256) void k_q4_rows(const Q4Args a, uint16_t* xp, u
                 }
                 *(u32x4*)(xp + n * Kp + kk) = o;
             } else {
-                sum = stage8<XT>(a.x, n * a.ldx + kk, ok, (char*)(xp + n * Kp + kk), plane * 2);
+                sum = place8<XT>(load8<XT>(a.x, n * a.ldx + kk, ok), (char*)(xp + n * Kp + kk), plane * 2);
             }
         }
 #pragma unroll
@@ -819,33 +865,33 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
 }
 
 constexpr int kMaxDim = 1 << 30;   // row and column indices of a tile stay in 32 bits
-constexpr int kQ4Lds = 44 * 1024;   // staged activations of a workgroup
 
 size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 int launch_status() { return hipGetLastError() == hipSuccess ? SEEDMM_OK : SEEDMM_EHIP; }
 
-template <int XT, bool SF32, int GROUP, int JN, int WAVES, int KW>
+template <int XT, bool SF32, int GROUP, int JN, int WAVES, int KW, int SS>
 void launch_q4_kw(const Q4Args& a, hipStream_t st) {
     constexpr int EB = XT == SEEDMM_I8 ? 1 : 2, PL = XT == SEEDMM_F32 ? 3 : 1;
     // the activation rows of a slab of columns in LDS, all columns if they fit
-    const int rows = a.N * PL;
-    const int per = 128 * EB * rows + 128 / GROUP * (JN == 1 ? 4 : 16) * 4;   // bytes of 128 columns
-    int slab = (kQ4Lds - rows * 16) / per * 128;
-    const int kround = (a.K + 127) / 128 * 128;
+    const int rows = a.N * PL, unit = 128 * SS;
+    const int per = unit * EB * rows + unit / GROUP * (JN == 1 ? 4 : 16) * 4;   // bytes of a unit of columns
+    constexpr int room = 62 * 1024 - KW * (WAVES / KW) * JN * 4 * 17 * 4 - (SS == 4 ? WAVES * 4096 : 0);
+    int slab = (room - rows * 16) / per * unit;
+    const int kround = (a.K + unit - 1) / unit * unit;
     if (slab > kround) slab = kround;
-    const size_t lds = (size_t)slab / 128 * per + rows * 16;
+    const size_t lds = (size_t)slab / unit * per + rows * 16;
     const int64_t tiles = ((int64_t)a.M + 15) / 16;
     const dim3 grid((unsigned)((tiles + WAVES / KW - 1) / (WAVES / KW)));
-    hipLaunchKernelGGL((k_q4<XT, SF32, GROUP, JN, WAVES, KW>), grid, dim3(WAVES * 64), lds, st, a, slab);
+    hipLaunchKernelGGL((k_q4<XT, SF32, GROUP, JN, WAVES, KW, SS>), grid, dim3(WAVES * 64), lds, st, a, slab);
 }
 
 template <int XT, bool SF32, int GROUP, int JN>
 void launch_q4_jn(const Q4Args& a, hipStream_t st) {
     const int64_t tiles = ((int64_t)a.M + 15) / 16;
-    if (tiles >= 4096) launch_q4_kw<XT, SF32, GROUP, JN, 8, 1>(a, st);
-    else if (tiles >= 256) launch_q4_kw<XT, SF32, GROUP, JN, 8, 4>(a, st);
-    else launch_q4_kw<XT, SF32, GROUP, JN, 16, 16>(a, st);
+    if (tiles >= 1024) launch_q4_kw<XT, SF32, GROUP, JN, 4, 1, 4>(a, st);
+    else if (tiles >= 256) launch_q4_kw<XT, SF32, GROUP, JN, 4, 4, 4>(a, st);
+    else launch_q4_kw<XT, SF32, GROUP, JN, 16, 16, 1>(a, st);
 }
 
 // The plan of a product with many tokens: what its workspace holds.
