@@ -31,6 +31,8 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float f) { return __builtin_bit_
 //     rows of the same instruction.
 //   int8 x: the integer instruction; D is exact.
 // ----------------------------------------------------------------------------------
+constexpr int kQ4Waves = 8;      // of a workgroup for a few tokens
+
 struct Q4Args {
     const uint32_t* w;   // [M][K/8], code k of a row in word k/8, bits 4 (k%8)
     const void* s;       // [M][K/group]
@@ -184,23 +186,26 @@ __device__ __forceinline__ float place8(const Raw8<XT>& x, char* dst, int64_t ro
 }
 
 // A few tokens.  A wave takes 16 weight rows; KW waves of a workgroup share a row tile and
-// take its slabs of SS * 128 columns in turn, each loaded while the one before is
-// multiplied, the first before the activations are staged.
-//   SS = 1: each lane loads the 16 bytes that it multiplies (a row's 64 bytes by 4 lanes).
-//   SS = 4: 16 lanes load 256 bytes of a row, whole cache lines, and the wave's own piece
-//     of LDS hands them to the lanes that multiply them.
+// take its slabs of 256 columns in turn, each loaded while the one before is multiplied,
+// the first before the activations are staged.  8 lanes load the 128 bytes of a row, whole
+// cache lines, and the wave's own piece of LDS hands them to the lanes that multiply them
+// (each lane loading its own 16 bytes, 64 bytes a row, took 54 us for 131072 x 2048 at one
+// token against 30 us: the texture path passes one line at a time).  That size streams
+// its 152 MB at 5.0 TB/s, what a large copy reaches; small matrices are bound by the
+// latency of one launch and two dependent loads (100 x 2048: 3.4 us, 2048 x 2048: 3.5 us).
 // The D tile of 16x16x32 instructions has a row a token: up to 4 activation rows sit in D
 // rows 0, 4, 8, 12 (JN = 1), so each lane scales one value a group instead of four.
-template <int XT, bool SF32, int GROUP, int JN, int WAVES, int KW, int SS>
-__global__ __launch_bounds__(WAVES * 64) void k_q4(const Q4Args a, int slab) {
+template <int XT, bool SF32, int GROUP, int JN, int KW>
+__global__ __launch_bounds__(kQ4Waves * 64) void k_q4(const Q4Args a, int slab) {
     constexpr int PL = XT == SEEDMM_F32 ? 3 : 1;       // operand rows a token
     constexpr int EB = XT == SEEDMM_I8 ? 1 : 2;
     constexpr int NG = 128 / GROUP;                    // groups of 128 columns
-    constexpr int RW = WAVES / KW;
+    constexpr int WAVES = kQ4Waves, RW = WAVES / KW, SS = 2;
     constexpr int SXW = JN == 1 ? 4 : 16;
     constexpr int SC = SS * 128;                       // columns of a wave's slab
     __shared__ float red[KW][RW][JN * 4][17];
-    __shared__ u32x4 bounce[SS == 4 ? WAVES : 1][SS == 4 ? 256 : 1];
+    constexpr int CR = 4 * SS;                         // 16-byte pieces of a row in it
+    __shared__ u32x4 bounce[WAVES][16 * CR];
     extern __shared__ __align__(16) char lds[];
     const int rowb = slab * EB + 16;
     float* sx = (float*)lds;                                     // [slab / GROUP][SXW]
@@ -214,11 +219,11 @@ __global__ __launch_bounds__(WAVES * 64) void k_q4(const Q4Args a, int slab) {
     const int64_t row = m0 + r < a.M ? m0 + r : a.M - 1;
     const int G = a.K / GROUP;
     // this lane's piece of load i: row lrow[i], columns 32 lcol ..
-    const int lcol = SS == 4 ? r : q;
+    const int lcol = lane % CR, lsub = lane / CR;
     const uint32_t* lrow[SS];
 #pragma unroll
     for (int i = 0; i < SS; ++i) {
-        const int64_t m = SS == 4 ? m0 + 4 * i + q : m0 + r;
+        const int64_t m = m0 + 16 / SS * i + lsub;
         lrow[i] = a.w + (m < a.M ? m : a.M - 1) * (a.K / 8);
     }
     const int xrow = JN == 1 ? min(r >> 2, rows - 1) : min(r, rows - 1);
@@ -309,17 +314,16 @@ __global__ __launch_bounds__(WAVES * 64) void k_q4(const Q4Args a, int slab) {
         for (int c0 = kw * SC; c0 < kn; c0 += KW * SC) {
             const Scales<SF32, NG * SS> sc = ss, bc = bs;
             u32x4 v[SS];
-            if constexpr (SS == 4) {
-                u32x4* const bw = bounce[wave];
+            u32x4* const bw = bounce[wave];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) bw[(4 * i + q) * 16 + (r ^ (4 * i + q))] = w[i];
-                wave_order();
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = bw[r * 16 + ((4 * j + q) ^ r)];
-                wave_order();
-            } else {
-                v[0] = w[0];
+            for (int i = 0; i < SS; ++i) {
+                const int lr = 16 / SS * i + lsub;
+                bw[lr * CR + (lcol ^ (lr & (CR - 1)))] = w[i];
             }
+            wave_order();
+#pragma unroll
+            for (int j = 0; j < SS; ++j) v[j] = bw[r * CR + ((4 * j + q) ^ (r & (CR - 1)))];
+            wave_order();
             if (c0 + KW * SC < kn) load(c0 + KW * SC);
 #pragma unroll
             for (int j = 0; j < SS; ++j)
@@ -870,28 +874,31 @@ size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 int launch_status() { return hipGetLastError() == hipSuccess ? SEEDMM_OK : SEEDMM_EHIP; }
 
-template <int XT, bool SF32, int GROUP, int JN, int WAVES, int KW, int SS>
+template <int XT, bool SF32, int GROUP, int JN, int KW>
 void launch_q4_kw(const Q4Args& a, hipStream_t st) {
-    constexpr int EB = XT == SEEDMM_I8 ? 1 : 2, PL = XT == SEEDMM_F32 ? 3 : 1;
+    constexpr int EB = XT == SEEDMM_I8 ? 1 : 2, PL = XT == SEEDMM_F32 ? 3 : 1, RW = kQ4Waves / KW;
     // the activation rows of a slab of columns in LDS, all columns if they fit
-    const int rows = a.N * PL, unit = 128 * SS;
+    const int rows = a.N * PL, unit = 256;
     const int per = unit * EB * rows + unit / GROUP * (JN == 1 ? 4 : 16) * 4;   // bytes of a unit of columns
-    constexpr int room = 62 * 1024 - KW * (WAVES / KW) * JN * 4 * 17 * 4 - (SS == 4 ? WAVES * 4096 : 0);
+    constexpr int room = 62 * 1024 - KW * RW * JN * 4 * 17 * 4 - kQ4Waves * 2048;
     int slab = (room - rows * 16) / per * unit;
     const int kround = (a.K + unit - 1) / unit * unit;
     if (slab > kround) slab = kround;
     const size_t lds = (size_t)slab / unit * per + rows * 16;
     const int64_t tiles = ((int64_t)a.M + 15) / 16;
-    const dim3 grid((unsigned)((tiles + WAVES / KW - 1) / (WAVES / KW)));
-    hipLaunchKernelGGL((k_q4<XT, SF32, GROUP, JN, WAVES, KW, SS>), grid, dim3(WAVES * 64), lds, st, a, slab);
+    hipLaunchKernelGGL((k_q4<XT, SF32, GROUP, JN, KW>), dim3((unsigned)((tiles + RW - 1) / RW)),
+                       dim3(kQ4Waves * 64), lds, st, a, slab);
 }
 
+// The fewer row tiles, the more waves share one (us with 2, 4, 8 waves, one bf16 token:
+// 131072 x 2048 30 33 39, 16384 x 8192 20 19 21, 8192 x 2048 6.0 5.1 5.1, 2048 x 2048
+// 5.7 4.2 3.5; 16 tokens: 51 69 105, 35 35 51, 8.7 7.7 8.3, 7.8 6.4 5.7).
 template <int XT, bool SF32, int GROUP, int JN>
 void launch_q4_jn(const Q4Args& a, hipStream_t st) {
     const int64_t tiles = ((int64_t)a.M + 15) / 16;
-    if (tiles >= 1024) launch_q4_kw<XT, SF32, GROUP, JN, 4, 1, 4>(a, st);
-    else if (tiles >= 256) launch_q4_kw<XT, SF32, GROUP, JN, 4, 4, 4>(a, st);
-    else launch_q4_kw<XT, SF32, GROUP, JN, 16, 16, 1>(a, st);
+    if (tiles >= 4096) launch_q4_kw<XT, SF32, GROUP, JN, 2>(a, st);
+    else if (tiles >= 512) launch_q4_kw<XT, SF32, GROUP, JN, 4>(a, st);
+    else launch_q4_kw<XT, SF32, GROUP, JN, 8>(a, st);
 }
 
 // The plan of a product with many tokens: what its workspace holds.
