@@ -713,8 +713,48 @@ __global__ __launch_bounds__(256) void k_q4_zero(void* y, int y_bf16, int ldy, i
 }
 
 // ----------------------------------------------------------------------------------
+// Reductions over a wave in vector registers: exchanges within 16 lanes (quads by 1 and 2,
+// then mirrored halves), then between the four 16-lane rows.
+// ----------------------------------------------------------------------------------
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+
+template <typename F>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, F f) {
+    v = f(v, dpp<0xB1>(v));    // lane ^ 1
+    v = f(v, dpp<0x4E>(v));    // lane ^ 2
+    v = f(v, dpp<0x141>(v));   // 7 - lane of 8
+    v = f(v, dpp<0x140>(v));   // 15 - lane of 16
+    auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = f(a[0], a[1]);
+    auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return f(b[0], b[1]);
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+    return __uint_as_float(wave_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
+}
+__device__ __forceinline__ float wave_max(float v) {
+    return __uint_as_float(wave_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }));
+}
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+    return wave_reduce(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+__device__ __forceinline__ uint32_t wave_umin(uint32_t v) {
+    return wave_reduce(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+
+// ----------------------------------------------------------------------------------
 // seedmm_add_norm.  r = x + delta in fp32; out = r rsqrt(mean r^2 + eps) w.  The 8-bit
-// scale is max |r w| times the row's factor over 127: one pass finds both statistics.
+// scale is max |r w| times the row's factor over 127: one pass finds both statistics, and
+// a row stays in registers between its load and its store (rows up to 32,768 elements;
+// longer ones are read twice).
 // ----------------------------------------------------------------------------------
 struct NormArgs {
     const void* x;
@@ -733,57 +773,210 @@ __device__ __forceinline__ float load_el(const void* p, int dt, int64_t i) {
     return dt == SEEDMM_F32 ? ((const float*)p)[i] : bf16_to_f32(((const uint16_t*)p)[i]);
 }
 
-__global__ __launch_bounds__(256) void k_add_norm(const NormArgs a) {
-    __shared__ float red[2][4];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
-        float ss = 0.f, top = 0.f;
-        bool bad = false;
-        for (int h = threadIdx.x; h < a.H; h += 256) {
-            float r = load_el(a.x, a.x_dt, n * a.ldx + h);
-            if (a.d) r += load_el(a.d, a.d_dt, n * a.ldd + h);
-            const float v = a.w ? r * load_el(a.w, a.w_dt, h) : r;
-            ss = __builtin_fmaf(r, r, ss);
-            top = fmaxf(top, fabsf(v));
-            bad |= !(fabsf(v) < INFINITY);
-        }
-        if (bad) top = INFINITY;
+// 8 elements from index i, of which the first n (1 .. 8) exist (the others read as 0).  The
+// vector accesses need the alignment of one element only.
+template <int DT>
+struct Eight {
+    uint32_t u[DT == SEEDMM_F32 ? 8 : 4];
+    __device__ __forceinline__ void load(const void* p, int64_t i, int n) {
+        const char* at = (const char*)p + i * (DT == SEEDMM_F32 ? 4 : 2);
+        if (n >= 8) {
+            __builtin_memcpy(u, at, sizeof(u));
+        } else {
 #pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
-            ss += __shfl_xor(ss, o);
-            top = fmaxf(top, __shfl_xor(top, o));
+            for (int j = 0; j < (int)(sizeof(u) / 4); ++j) u[j] = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < n) {
+                    if constexpr (DT == SEEDMM_F32) u[j] = ((const uint32_t*)at)[j];
+                    else u[j / 2] |= (uint32_t)((const uint16_t*)at)[j] << (16 * (j & 1));
+                }
         }
-        if (lane == 0) { red[0][wave] = ss; red[1][wave] = top; }
-        __syncthreads();
-        ss = (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]);
-        top = fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3]));
-        __syncthreads();
-        const float f = 1.0f / sqrtf(ss / (float)a.H + a.eps);
-        float sc = 0.f, inv = 0.f;
-        if (a.out_dt == SEEDMM_I8) {
-            sc = fmaxf(top * f / 127.0f, 1.17549435e-38f);
-            // a row with an infinity or NaN: codes 0 and scale NaN
-            if (!(top * f < INFINITY)) sc = NAN;
-            inv = sc == sc ? 1.0f / sc : 0.f;
-            if (threadIdx.x == 0) a.scale[n] = sc;
+    }
+    __device__ __forceinline__ float get(int j) const {
+        if constexpr (DT == SEEDMM_F32) return __uint_as_float(u[j]);
+        else return __uint_as_float((j & 1) ? u[j / 2] & 0xFFFF0000u : u[j / 2] << 16);
+    }
+};
+
+template <int DT>
+__device__ __forceinline__ void store8(void* p, int64_t i, int n, const float (&v)[8]) {
+    constexpr int B = DT == SEEDMM_F32 ? 4 : DT == SEEDMM_BF16 ? 2 : 1;
+    uint32_t u[2 * B];
+    if constexpr (DT == SEEDMM_F32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(v[j]);
+    } else if constexpr (DT == SEEDMM_BF16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] = (uint32_t)f32_to_bf16(v[2 * j]) | (uint32_t)f32_to_bf16(v[2 * j + 1]) << 16;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            u[j] = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[j] |= ((uint32_t)(int)v[4 * j + k] & 255u) << (8 * k);
         }
-        for (int h = threadIdx.x; h < a.H; h += 256) {
-            float r = load_el(a.x, a.x_dt, n * a.ldx + h);
-            if (a.d) r += load_el(a.d, a.d_dt, n * a.ldd + h);
-            const float v = (a.w ? r * load_el(a.w, a.w_dt, h) : r) * f;
-            if (a.res) {
-                if (a.x_dt == SEEDMM_F32) ((float*)a.res)[n * a.ldr + h] = r;
-                else ((uint16_t*)a.res)[n * a.ldr + h] = f32_to_bf16(r);
+    }
+    char* at = (char*)p + i * B;
+    if (n >= 8) {
+        __builtin_memcpy(at, u, sizeof(u));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n) {
+                if constexpr (DT == SEEDMM_F32) ((uint32_t*)at)[j] = u[j];
+                else if constexpr (DT == SEEDMM_BF16) ((uint16_t*)at)[j] = (uint16_t)(u[j / 2] >> (16 * (j & 1)));
+                else ((uint8_t*)at)[j] = (uint8_t)(u[j / 4] >> (8 * (j & 3)));
             }
-            if (a.out_dt == SEEDMM_I8) {
-                const float c = inv == 0.f ? 0.f : fminf(fmaxf(rintf(v * inv), -127.f), 127.f);
-                ((int8_t*)a.out)[n * a.ldo + h] = (int8_t)(int)c;
-            } else if (a.out_dt == SEEDMM_F32) {
-                ((float*)a.out)[n * a.ldo + h] = v;
+    }
+}
+
+// The row's factor, and for 8 bits its scale and the scale's reciprocal (0: codes 0).
+struct RowFactor {
+    float f, sc, inv;
+};
+__device__ __forceinline__ RowFactor row_factor(const NormArgs& a, float ss, float top) {
+    RowFactor o;
+    o.f = 1.0f / sqrtf(ss / (float)a.H + a.eps);
+    o.sc = o.inv = 0.f;
+    if (a.out_dt == SEEDMM_I8) {
+        o.sc = fmaxf(top * o.f / 127.0f, 1.17549435e-38f);
+        // a row with an infinity or NaN: codes 0 and scale NaN
+        if (!(top * o.f < INFINITY)) o.sc = NAN;
+        o.inv = o.sc == o.sc ? 1.0f / o.sc : 0.f;
+    }
+    return o;
+}
+__device__ __forceinline__ float code_of(float v, float inv) {
+    return inv == 0.f ? 0.f : fminf(fmaxf(rintf(v * inv), -127.f), 127.f);
+}
+
+// TPR threads a row (a wave, or a workgroup), NP pieces of 8 elements a thread.
+template <int TPR, int NP, int XT, int DT>   // DT: -1 = no delta
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_add_norm(const NormArgs a) {
+    constexpr int NW = TPR / 64;
+    __shared__ float red[2][NW];
+    const int tid = TPR < 256 ? threadIdx.x % TPR : threadIdx.x;
+    const int64_t n = TPR < 256 ? (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR : blockIdx.x;
+    if (n >= a.N) return;      // (a whole wave; workgroups of one row all have it)
+    Eight<XT> x[NP];
+    Eight<DT < 0 ? SEEDMM_BF16 : DT> d[NP];
+    int cnt[NP];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        const int h = (p * TPR + tid) * 8;
+        cnt[p] = min(8, a.H - h);
+        if (cnt[p] > 0) {
+            x[p].load(a.x, n * a.ldx + h, cnt[p]);
+            if constexpr (DT >= 0) d[p].load(a.d, n * a.ldd + h, cnt[p]);
+        }
+    }
+    float w[NP][8];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        const int h = (p * TPR + tid) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[p][j] = 1.f;
+        if (a.w && cnt[p] > 0) {
+            if (a.w_dt == SEEDMM_F32) {
+                Eight<SEEDMM_F32> e;
+                e.load(a.w, h, cnt[p]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[p][j] = e.get(j);
             } else {
-                ((uint16_t*)a.out)[n * a.ldo + h] = f32_to_bf16(v);
+                Eight<SEEDMM_BF16> e;
+                e.load(a.w, h, cnt[p]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[p][j] = e.get(j);
             }
         }
+    }
+    float r[NP][8], ss = 0.f, top = 0.f;
+    bool bad = false;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float v = 0.f;
+            if (cnt[p] > 0) {
+                v = x[p].get(j);
+                if constexpr (DT >= 0) v += d[p].get(j);
+            }
+            r[p][j] = v;
+            ss = __builtin_fmaf(v, v, ss);
+        }
+        if (a.res && cnt[p] > 0) store8<XT>(a.res, n * a.ldr + (p * TPR + tid) * 8, cnt[p], r[p]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            r[p][j] *= w[p][j];
+            top = fmaxf(top, fabsf(r[p][j]));
+            bad |= !(fabsf(r[p][j]) < INFINITY);
+        }
+    }
+    ss = wave_sum(ss);
+    if (a.out_dt == SEEDMM_I8) top = wave_max(bad ? INFINITY : top);
+    if constexpr (NW > 1) {
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) { red[0][wave] = ss; red[1][wave] = top; }
+        __syncthreads();
+        ss = red[0][0]; top = red[1][0];
+#pragma unroll
+        for (int i = 1; i < NW; ++i) { ss += red[0][i]; top = fmaxf(top, red[1][i]); }
+    }
+    const RowFactor o = row_factor(a, ss, top);
+    if (a.out_dt == SEEDMM_I8 && tid == 0) a.scale[n] = o.sc;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        if (cnt[p] <= 0) continue;
+        const int64_t at = n * a.ldo + (p * TPR + tid) * 8;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = r[p][j] * o.f;
+        if (a.out_dt == SEEDMM_I8) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = code_of(v[j], o.inv);
+            store8<SEEDMM_I8>(a.out, at, cnt[p], v);
+        } else if (a.out_dt == SEEDMM_F32) {
+            store8<SEEDMM_F32>(a.out, at, cnt[p], v);
+        } else {
+            store8<SEEDMM_BF16>(a.out, at, cnt[p], v);
+        }
+    }
+}
+
+// Rows of any length, read twice.
+__global__ __launch_bounds__(1024) void k_add_norm_long(const NormArgs a) {
+    __shared__ float red[2][16];
+    const int64_t n = blockIdx.x;
+    float ss = 0.f, top = 0.f;
+    bool bad = false;
+    for (int h = threadIdx.x; h < a.H; h += 1024) {
+        float r = load_el(a.x, a.x_dt, n * a.ldx + h);
+        if (a.d) r += load_el(a.d, a.d_dt, n * a.ldd + h);
+        const float v = a.w ? r * load_el(a.w, a.w_dt, h) : r;
+        ss = __builtin_fmaf(r, r, ss);
+        top = fmaxf(top, fabsf(v));
+        bad |= !(fabsf(v) < INFINITY);
+    }
+    ss = wave_sum(ss);
+    top = wave_max(bad ? INFINITY : top);
+    if ((threadIdx.x & 63) == 0) { red[0][threadIdx.x >> 6] = ss; red[1][threadIdx.x >> 6] = top; }
+    __syncthreads();
+    ss = red[0][0]; top = red[1][0];
+    for (int i = 1; i < 16; ++i) { ss += red[0][i]; top = fmaxf(top, red[1][i]); }
+    const RowFactor o = row_factor(a, ss, top);
+    if (a.out_dt == SEEDMM_I8 && threadIdx.x == 0) a.scale[n] = o.sc;
+    for (int h = threadIdx.x; h < a.H; h += 1024) {
+        float r = load_el(a.x, a.x_dt, n * a.ldx + h);
+        if (a.d) r += load_el(a.d, a.d_dt, n * a.ldd + h);
+        const float v = (a.w ? r * load_el(a.w, a.w_dt, h) : r) * o.f;
+        if (a.res) {
+            if (a.x_dt == SEEDMM_F32) ((float*)a.res)[n * a.ldr + h] = r;
+            else ((uint16_t*)a.res)[n * a.ldr + h] = f32_to_bf16(r);
+        }
+        if (a.out_dt == SEEDMM_I8) ((int8_t*)a.out)[n * a.ldo + h] = (int8_t)(int)code_of(v, o.inv);
+        else if (a.out_dt == SEEDMM_F32) ((float*)a.out)[n * a.ldo + h] = v;
+        else ((uint16_t*)a.out)[n * a.ldo + h] = f32_to_bf16(v);
     }
 }
 
@@ -791,6 +984,11 @@ __global__ __launch_bounds__(256) void k_add_norm(const NormArgs a) {
 // seedmm_route.  One wave a token: the largest key of the E logits, top_k times.  A key
 // orders the eligible scores above 1, the ineligible experts (logit NaN or -inf) at 1 and
 // the chosen ones at 0; equal keys go to the lower expert.
+//
+// Sigmoid scores are compared in 64 bits, but only where it matters: the top_k-th largest
+// of the fp32 scores bounds the choice, and the experts that reach it within the fp32
+// scores' error (one a lane) are scored again in 64 bits and ordered.  Where more than 64
+// experts are that near, or fewer than top_k are eligible, all are.
 // ----------------------------------------------------------------------------------
 struct RouteArgs {
     const void* lg;
@@ -801,67 +999,169 @@ struct RouteArgs {
     int T, E, k, l_dt;
 };
 
-// order-preserving unsigned key of a float (-0 equals +0); -inf maps above 1
-__device__ __forceinline__ uint64_t key_of(double f) {
+// order-preserving unsigned keys (-0 equals +0; every number above -inf is above 1)
+__device__ __forceinline__ uint32_t key32(float f) {
+    const uint32_t u = __float_as_uint(f + 0.0f);
+    return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float unkey32(uint32_t k) {
+    return __uint_as_float((k >> 31) ? k & 0x7FFFFFFFu : ~k);
+}
+__device__ __forceinline__ uint64_t key64(double f) {
     const uint64_t u = (uint64_t)__double_as_longlong(f + 0.0);
     return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
+__device__ __forceinline__ double sigmoid64(float l) { return 1.0 / (1.0 + exp(-(double)l)); }
 
-template <int NPL, bool SIG>
+// The largest key of the wave and the lowest expert i * 64 + lane that has it.
+template <int NPL>
+__device__ __forceinline__ uint32_t largest(const uint32_t (&key)[NPL], int lane, int& e) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < NPL; ++i) best = max(best, key[i]);
+    best = wave_umax(best);
+    e = -1;
+    if constexpr (NPL <= 8) {
+#pragma unroll
+        for (int i = NPL - 1; i >= 0; --i) {
+            const uint64_t m = __ballot(key[i] == best);
+            if (m) e = i * 64 + __builtin_ctzll(m);
+        }
+    } else {
+        uint32_t at = 0xFFFFFFFFu;
+#pragma unroll
+        for (int i = NPL - 1; i >= 0; --i)
+            if (key[i] == best) at = i * 64 + lane;
+        e = (int)wave_umin(at);
+    }
+    return best;
+}
+template <int NPL>
+__device__ __forceinline__ uint64_t largest(const uint64_t (&key)[NPL], int lane, int& e) {
+    uint64_t mine = key[0];
+    int at = 0;
+#pragma unroll
+    for (int i = 1; i < NPL; ++i)
+        if (key[i] > mine) { mine = key[i]; at = i; }
+    const uint32_t hi = wave_umax((uint32_t)(mine >> 32));
+    const uint32_t lo = wave_umax((uint32_t)(mine >> 32) == hi ? (uint32_t)mine : 0u);
+    const uint64_t best = (uint64_t)hi << 32 | lo;
+    e = (int)wave_umin(mine == best ? (uint32_t)(at * 64 + lane) : 0xFFFFFFFFu);
+    return best;
+}
+template <int NPL, typename K>
+__device__ __forceinline__ void clear_key(K (&key)[NPL], int lane, int e) {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+        if (i * 64 + lane == e) key[i] = 0;
+}
+
+template <int NPL, bool SIG, int LT>
 __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
     const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (t >= a.T) return;
-    uint64_t key[NPL];
+    float l[NPL], bias[SIG ? NPL : 1];
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         const int e = i * 64 + lane;
-        key[i] = 0;
-        if (e < a.E) {
-            const float l = load_el(a.lg, a.l_dt, t * a.ldl + e);
-            double v = l;
-            if constexpr (SIG) {
-                v = 1.0 / (1.0 + exp(-(double)l));
-                if (a.bias) v += (double)a.bias[e];
-            }
-            key[i] = (l > -INFINITY && v > -INFINITY) ? key_of(v) : 1;
-        }
+        l[i] = e < a.E ? load_el(a.lg, LT, t * a.ldl + e) : 0.f;
+        if constexpr (SIG) bias[i] = e < a.E && a.bias ? a.bias[e] : 0.f;
     }
     int mine = 0;         // lane s < k keeps slot s
+    float ml = -INFINITY;
     bool elig = false;
-    for (int s = 0; s < a.k; ++s) {
-        uint64_t best = 0;
-        int at = 0;
+    uint32_t key[NPL];
 #pragma unroll
-        for (int i = 0; i < NPL; ++i)
-            if (key[i] > best) { best = key[i]; at = i; }
-        int e = at * 64 + lane;
-#pragma unroll
-        for (int o = 1; o < 64; o *= 2) {
-            const uint64_t ob = __shfl_xor((unsigned long long)best, o);
-            const int oe = __shfl_xor(e, o);
-            if (ob > best || (ob == best && oe < e)) { best = ob; e = oe; }
-        }
-#pragma unroll
-        for (int i = 0; i < NPL; ++i)
-            if (i * 64 + lane == e) key[i] = 0;
-        if (lane == s) { mine = e; elig = best > 1; }
+    for (int i = 0; i < NPL; ++i) {
+        float v = l[i];
+        if constexpr (SIG) v = 1.0f / (1.0f + expf(-l[i])) + bias[i];
+        key[i] = i * 64 + lane >= a.E ? 0u : l[i] > -INFINITY && v > -INFINITY ? key32(v) : 1u;
     }
-    float l = -INFINITY;
-    if (lane < a.k && elig) l = load_el(a.lg, a.l_dt, t * a.ldl + mine);
+    if constexpr (!SIG) {
+        for (int s = 0; s < a.k; ++s) {
+            int e;
+            const uint32_t best = largest<NPL>(key, lane, e);
+            clear_key<NPL>(key, lane, e);
+            if (lane == s) { mine = e; elig = best > 1; ml = unkey32(best); }
+        }
+    } else {
+        uint32_t rest[NPL], best = 0;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) rest[i] = key[i];
+        for (int s = 0; s < a.k; ++s) {
+            int e;
+            best = largest<NPL>(rest, lane, e);
+            clear_key<NPL>(rest, lane, e);
+        }
+        // fp32 scores are off by less than 2^-22 + 2^-24 |score|
+        const float kth = unkey32(best), low = kth - 9.5367431640625e-7f * (1.0f + fabsf(kth));
+        bool near[NPL];
+        int count = 0;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            const float v = unkey32(key[i]);
+            near[i] = key[i] > 1 && (v >= kth || v >= low);
+            count += __popcll(__ballot(near[i]));
+        }
+        if (best > 1 && count <= 64) {
+            // candidate c goes to lane c
+            int ce = -1, base = 0;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+                const uint64_t m = __ballot(near[i]);
+                const int nm = __popcll(m);
+                // lane base + j takes the j-th set bit
+                int j = lane - base;
+                if (j >= 0 && j < nm) {
+                    uint64_t x = m;
+                    int pos = 0;
+#pragma unroll
+                    for (int w = 32; w >= 1; w >>= 1) {
+                        const uint64_t part = x & ((1ull << w) - 1);
+                        const int c = __popcll(part);
+                        if (j >= c) { j -= c; x >>= w; pos += w; }
+                        else x = part;
+                    }
+                    ce = i * 64 + pos;
+                }
+                base += nm;
+            }
+            const float cl = ce >= 0 ? load_el(a.lg, LT, t * a.ldl + ce) : 0.f;
+            const float cb = ce >= 0 && a.bias ? a.bias[ce] : 0.f;
+            uint64_t ck[1] = {ce >= 0 ? key64(sigmoid64(cl) + (double)cb) : 0};
+            for (int s = 0; s < a.k; ++s) {
+                int c;
+                largest<1>(ck, lane, c);      // candidates are in the experts' order
+                const int e = __builtin_amdgcn_readlane(ce, c);
+                const float el = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(cl), c));
+                clear_key<1>(ck, lane, c);
+                if (lane == s) { mine = e; elig = true; ml = el; }
+            }
+        } else {
+            uint64_t k64[NPL];
+#pragma unroll
+            for (int i = 0; i < NPL; ++i)
+                k64[i] = key[i] > 1 ? key64(sigmoid64(l[i]) + (double)bias[i]) : key[i];
+            for (int s = 0; s < a.k; ++s) {
+                int e;
+                const uint64_t top = largest<NPL>(k64, lane, e);
+                clear_key<NPL>(k64, lane, e);
+                if (lane == s) { mine = e; elig = top > 1; }
+            }
+            if (lane < a.k && elig) ml = load_el(a.lg, LT, t * a.ldl + mine);
+        }
+    }
+    if (lane >= a.k || !elig) ml = -INFINITY;
     float w;
     if constexpr (SIG) {
-        w = (float)(1.0 / (1.0 + exp(-(double)l)));
+        w = (float)sigmoid64(ml);
     } else {
-        float top = l;
-#pragma unroll
-        for (int o = 1; o < 64; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
-        w = l == top ? 1.0f : expf(l - top);
+        const float top = wave_max(ml);
+        w = ml == top ? 1.0f : expf(ml - top);
     }
     if (!elig || lane >= a.k) w = 0.f;
-    float sum = w;
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) sum += __shfl_xor(sum, o);
+    const float sum = wave_sum(w);
     if (lane < a.k) {
         a.ids[t * a.k + lane] = mine;
         a.w[t * a.k + lane] = sum > 0.f ? w / sum : 0.f;
@@ -970,16 +1270,34 @@ void launch_q4(const Q4Args& a, int group, const Q4Plan& p, void* ws, hipStream_
     else launch_q4_group<XT, SF32, 128>(a, p, ws, st);
 }
 
-template <bool SIG>
+template <bool SIG, int LT>
 void launch_route(const RouteArgs& a, hipStream_t st) {
     const dim3 grid((unsigned)((a.T - 1) / 4 + 1)), block(256);
-    if (a.E <= 64) hipLaunchKernelGGL((k_route<1, SIG>), grid, block, 0, st, a);
-    else if (a.E <= 128) hipLaunchKernelGGL((k_route<2, SIG>), grid, block, 0, st, a);
-    else if (a.E <= 256) hipLaunchKernelGGL((k_route<4, SIG>), grid, block, 0, st, a);
-    else if (a.E <= 512) hipLaunchKernelGGL((k_route<8, SIG>), grid, block, 0, st, a);
-    else if (a.E <= 1024) hipLaunchKernelGGL((k_route<16, SIG>), grid, block, 0, st, a);
-    else if (a.E <= 2048) hipLaunchKernelGGL((k_route<32, SIG>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((k_route<64, SIG>), grid, block, 0, st, a);
+    if (a.E <= 64) hipLaunchKernelGGL((k_route<1, SIG, LT>), grid, block, 0, st, a);
+    else if (a.E <= 128) hipLaunchKernelGGL((k_route<2, SIG, LT>), grid, block, 0, st, a);
+    else if (a.E <= 256) hipLaunchKernelGGL((k_route<4, SIG, LT>), grid, block, 0, st, a);
+    else if (a.E <= 512) hipLaunchKernelGGL((k_route<8, SIG, LT>), grid, block, 0, st, a);
+    else if (a.E <= 1024) hipLaunchKernelGGL((k_route<16, SIG, LT>), grid, block, 0, st, a);
+    else if (a.E <= 2048) hipLaunchKernelGGL((k_route<32, SIG, LT>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((k_route<64, SIG, LT>), grid, block, 0, st, a);
+}
+
+template <int TPR, int NP, int XT, int DT>
+void launch_norm_as(const NormArgs& a, hipStream_t st) {
+    const int rows = TPR < 256 ? 256 / TPR : 1;
+    hipLaunchKernelGGL((k_add_norm<TPR, NP, XT, DT>), dim3((unsigned)((a.N - 1) / rows + 1)),
+                       dim3(TPR < 256 ? 256 : TPR), 0, st, a);
+}
+
+template <int XT, int DT>
+void launch_norm(const NormArgs& a, hipStream_t st) {
+    if (a.H <= 512) launch_norm_as<64, 1, XT, DT>(a, st);
+    else if (a.H <= 2048) launch_norm_as<256, 1, XT, DT>(a, st);
+    else if (a.H <= 4096) launch_norm_as<256, 2, XT, DT>(a, st);
+    else if (a.H <= 8192) launch_norm_as<256, 4, XT, DT>(a, st);
+    else if (a.H <= 16384) launch_norm_as<1024, 2, XT, DT>(a, st);
+    else if (a.H <= 32768) launch_norm_as<1024, 4, XT, DT>(a, st);
+    else hipLaunchKernelGGL(k_add_norm_long, dim3((unsigned)a.N), dim3(1024), 0, st, a);
 }
 
 bool float_type(int dt) { return dt == SEEDMM_F32 || dt == SEEDMM_BF16; }
@@ -1052,7 +1370,11 @@ int seedmm_add_norm(const void* x, int x_dtype, int64_t ldx, const void* delta, 
         return SEEDMM_EALIGN;
     NormArgs a = {x, delta, weight, residual, out, scale, x_dtype, delta_dtype, w_dtype, out_dtype,
                   ldx, ldd, ldr, ldo, N, H, eps};
-    hipLaunchKernelGGL(k_add_norm, dim3((unsigned)N), dim3(256), 0, (hipStream_t)hip_stream, a);
+    hipStream_t st = (hipStream_t)hip_stream;
+    const bool xf = x_dtype == SEEDMM_F32, df = delta_dtype == SEEDMM_F32;
+    if (!delta) xf ? launch_norm<SEEDMM_F32, -1>(a, st) : launch_norm<SEEDMM_BF16, -1>(a, st);
+    else if (df) xf ? launch_norm<SEEDMM_F32, SEEDMM_F32>(a, st) : launch_norm<SEEDMM_BF16, SEEDMM_F32>(a, st);
+    else xf ? launch_norm<SEEDMM_F32, SEEDMM_BF16>(a, st) : launch_norm<SEEDMM_BF16, SEEDMM_BF16>(a, st);
     return launch_status();
 }
 
@@ -1068,8 +1390,10 @@ int seedmm_route(const void* logits, int l_dtype, int64_t ldl, const float* bias
         ((uintptr_t)ids & 3) || ((uintptr_t)w & 3))
         return SEEDMM_EALIGN;
     RouteArgs a = {logits, bias, ids, w, ldl, T, E, top_k, l_dtype};
-    if (score == SEEDMM_SIGMOID) launch_route<true>(a, (hipStream_t)hip_stream);
-    else launch_route<false>(a, (hipStream_t)hip_stream);
+    hipStream_t st = (hipStream_t)hip_stream;
+    const bool lf = l_dtype == SEEDMM_F32;
+    if (score == SEEDMM_SIGMOID) lf ? launch_route<true, SEEDMM_F32>(a, st) : launch_route<true, SEEDMM_BF16>(a, st);
+    else lf ? launch_route<false, SEEDMM_F32>(a, st) : launch_route<false, SEEDMM_BF16>(a, st);
     return launch_status();
 }
 
