@@ -981,14 +981,16 @@ __global__ __launch_bounds__(1024) void k_add_norm_long(const NormArgs a) {
 }
 
 // ----------------------------------------------------------------------------------
-// seedmm_route.  One wave a token: the largest key of the E logits, top_k times.  A key
-// orders the eligible scores above 1, the ineligible experts (logit NaN or -inf) at 1 and
-// the chosen ones at 0; equal keys go to the lower expert.
+// seedmm_route.  One wave a token, expert i * 64 + lane in register i.  A key orders the
+// eligible scores above 1 and the ineligible experts (logit NaN or -inf) at 1.
 //
-// Sigmoid scores are compared in 64 bits, but only where it matters: the top_k-th largest
-// of the fp32 scores bounds the choice, and the experts that reach it within the fp32
-// scores' error (one a lane) are scored again in 64 bits and ordered.  Where more than 64
-// experts are that near, or fewer than top_k are eligible, all are.
+// The top_k-th largest of the 64 lane maxima is a lower bound of the top_k-th largest key,
+// and few keys reach it (about top_k + 2 of 512 for top_k = 10).  Those go to a lane each,
+// through LDS, and every one's rank is the number of larger ones (equal: of lower experts):
+// rank s < top_k is slot s.  Sigmoid scores are compared in 64 bits, but bounded in fp32:
+// the bound is lowered by the fp32 scores' error, and only the candidates are scored again.
+// Where more than 64 reach the bound, or fewer than top_k lanes have an eligible expert,
+// the largest key is taken top_k times instead.
 // ----------------------------------------------------------------------------------
 struct RouteArgs {
     const void* lg;
@@ -1056,10 +1058,17 @@ __device__ __forceinline__ void clear_key(K (&key)[NPL], int lane, int e) {
         if (i * 64 + lane == e) key[i] = 0;
 }
 
+// sigmoid in fp32, off by less than 2^-22
+__device__ __forceinline__ float sigmoid32(float l) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l * -1.44269504088896f));
+}
+
 template <int NPL, bool SIG, int LT>
 __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
+    __shared__ int cand[4][64];
     const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t = (int64_t)blockIdx.x * 4 + wave;
     if (t >= a.T) return;
     float l[NPL], bias[SIG ? NPL : 1];
 #pragma unroll
@@ -1068,103 +1077,90 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
         l[i] = e < a.E ? load_el(a.lg, LT, t * a.ldl + e) : 0.f;
         if constexpr (SIG) bias[i] = e < a.E && a.bias ? a.bias[e] : 0.f;
     }
-    int mine = 0;         // lane s < k keeps slot s
-    float ml = -INFINITY;
-    bool elig = false;
-    uint32_t key[NPL];
+    uint32_t key[NPL], top[1] = {0};
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         float v = l[i];
-        if constexpr (SIG) v = 1.0f / (1.0f + expf(-l[i])) + bias[i];
+        if constexpr (SIG) v = sigmoid32(l[i]) + bias[i];
         key[i] = i * 64 + lane >= a.E ? 0u : l[i] > -INFINITY && v > -INFINITY ? key32(v) : 1u;
+        top[0] = max(top[0], key[i]);
     }
-    if constexpr (!SIG) {
+    uint32_t bound = 0;
+    for (int s = 0; s < a.k; ++s) {
+        int e;
+        bound = largest<1>(top, lane, e);
+        clear_key<1>(top, lane, e);
+    }
+    const bool all = bound <= 1;      // fewer than top_k lanes with an eligible expert
+    // fp32 scores are off by less than 2^-22 + 2^-24 |score|, two of them by twice that
+    if constexpr (SIG) {
+        const float b = unkey32(bound), low = b - 9.5367431640625e-7f * (1.0f + fabsf(b));
+        if (low > -INFINITY) bound = key32(low);
+    }
+    int count = 0;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const bool near = key[i] > 1 && key[i] >= bound;
+        const uint64_t m = __ballot(near);
+        const int at = count + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
+        if (near && at < 64) cand[wave][at] = i * 64 + lane;
+        count += __popcll(m);
+    }
+
+    int mine = 0, slot = -1;          // this lane's expert and its slot
+    float ml = -INFINITY;             // its logit, -inf if it is masked
+    if (!all && count <= 64) {
+        wave_order();
+        if (lane < count) {
+            mine = cand[wave][lane];
+            ml = load_el(a.lg, LT, t * a.ldl + mine);
+        }
+        uint64_t k64 = 0;
+        if (lane < count) {
+            if constexpr (SIG) k64 = key64(sigmoid64(ml) + (a.bias ? (double)a.bias[mine] : 0.0));
+            else k64 = key32(ml);
+        }
+        int rank = 0;
+        for (int c = 0; c < count; ++c) {   // candidates are in the experts' order
+            uint64_t o = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)k64, c);
+            if constexpr (SIG) o |= (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(k64 >> 32), c) << 32;
+            rank += o > k64 || (o == k64 && c < lane);
+        }
+        if (lane < count && rank < a.k) slot = rank;
+    } else if constexpr (SIG) {
+        uint64_t k64[NPL];
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            k64[i] = key[i] > 1 ? key64(sigmoid64(l[i]) + (double)bias[i]) : key[i];
+        for (int s = 0; s < a.k; ++s) {
+            int e;
+            const uint64_t best = largest<NPL>(k64, lane, e);
+            clear_key<NPL>(k64, lane, e);
+            if (lane == s) { mine = e; slot = s; ml = best > 1 ? 0.f : -INFINITY; }
+        }
+        if (slot >= 0 && ml == 0.f) ml = load_el(a.lg, LT, t * a.ldl + mine);
+    } else {
         for (int s = 0; s < a.k; ++s) {
             int e;
             const uint32_t best = largest<NPL>(key, lane, e);
             clear_key<NPL>(key, lane, e);
-            if (lane == s) { mine = e; elig = best > 1; ml = unkey32(best); }
-        }
-    } else {
-        uint32_t rest[NPL], best = 0;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) rest[i] = key[i];
-        for (int s = 0; s < a.k; ++s) {
-            int e;
-            best = largest<NPL>(rest, lane, e);
-            clear_key<NPL>(rest, lane, e);
-        }
-        // fp32 scores are off by less than 2^-22 + 2^-24 |score|
-        const float kth = unkey32(best), low = kth - 9.5367431640625e-7f * (1.0f + fabsf(kth));
-        bool near[NPL];
-        int count = 0;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            const float v = unkey32(key[i]);
-            near[i] = key[i] > 1 && (v >= kth || v >= low);
-            count += __popcll(__ballot(near[i]));
-        }
-        if (best > 1 && count <= 64) {
-            // candidate c goes to lane c
-            int ce = -1, base = 0;
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) {
-                const uint64_t m = __ballot(near[i]);
-                const int nm = __popcll(m);
-                // lane base + j takes the j-th set bit
-                int j = lane - base;
-                if (j >= 0 && j < nm) {
-                    uint64_t x = m;
-                    int pos = 0;
-#pragma unroll
-                    for (int w = 32; w >= 1; w >>= 1) {
-                        const uint64_t part = x & ((1ull << w) - 1);
-                        const int c = __popcll(part);
-                        if (j >= c) { j -= c; x >>= w; pos += w; }
-                        else x = part;
-                    }
-                    ce = i * 64 + pos;
-                }
-                base += nm;
-            }
-            const float cl = ce >= 0 ? load_el(a.lg, LT, t * a.ldl + ce) : 0.f;
-            const float cb = ce >= 0 && a.bias ? a.bias[ce] : 0.f;
-            uint64_t ck[1] = {ce >= 0 ? key64(sigmoid64(cl) + (double)cb) : 0};
-            for (int s = 0; s < a.k; ++s) {
-                int c;
-                largest<1>(ck, lane, c);      // candidates are in the experts' order
-                const int e = __builtin_amdgcn_readlane(ce, c);
-                const float el = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(cl), c));
-                clear_key<1>(ck, lane, c);
-                if (lane == s) { mine = e; elig = true; ml = el; }
-            }
-        } else {
-            uint64_t k64[NPL];
-#pragma unroll
-            for (int i = 0; i < NPL; ++i)
-                k64[i] = key[i] > 1 ? key64(sigmoid64(l[i]) + (double)bias[i]) : key[i];
-            for (int s = 0; s < a.k; ++s) {
-                int e;
-                const uint64_t top = largest<NPL>(k64, lane, e);
-                clear_key<NPL>(k64, lane, e);
-                if (lane == s) { mine = e; elig = top > 1; }
-            }
-            if (lane < a.k && elig) ml = load_el(a.lg, LT, t * a.ldl + mine);
+            if (lane == s) { mine = e; slot = s; ml = best > 1 ? unkey32(best) : -INFINITY; }
         }
     }
-    if (lane >= a.k || !elig) ml = -INFINITY;
+
+    const bool weighs = slot >= 0 && ml > -INFINITY;
     float w;
     if constexpr (SIG) {
         w = (float)sigmoid64(ml);
     } else {
-        const float top = wave_max(ml);
-        w = ml == top ? 1.0f : expf(ml - top);
+        const float m = wave_max(weighs ? ml : -INFINITY);
+        w = ml == m ? 1.0f : expf(ml - m);
     }
-    if (!elig || lane >= a.k) w = 0.f;
+    if (!weighs) w = 0.f;
     const float sum = wave_sum(w);
-    if (lane < a.k) {
-        a.ids[t * a.k + lane] = mine;
-        a.w[t * a.k + lane] = sum > 0.f ? w / sum : 0.f;
+    if (slot >= 0) {
+        a.ids[t * a.k + slot] = mine;
+        a.w[t * a.k + slot] = sum > 0.f ? w / sum : 0.f;
     }
 }
 
