@@ -613,38 +613,48 @@ _FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
 _ROWS = {torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8}
 
 
-def _row_tensor(t, types, name, dev=None):
-    """(dtype code, rows, columns, leading dimension) of a row-major GPU tensor [N][C] or
-    [C] whose rows may be apart (last dimension contiguous)."""
+def _refuse(t, types, name, dev):
+    """Why a tensor was not taken: not on a GPU, of another type, or on another device."""
     if not (isinstance(t, torch.Tensor) and t.is_cuda):
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    code = types.get(t.dtype)
-    if code is None:
+    if t.dtype not in types:
         raise TypeError(f"{name} must be one of {[str(d) for d in types]}, got {t.dtype}")
-    if dev is not None and t.get_device() != dev:
-        raise ValueError(f"{name} is on another device")
-    shape = t.shape
+    raise ValueError(f"{name} is on another device")
+
+
+# The checks run on every call of a decode step, so they ask a tensor for as little as they
+# can: device, type, shape and strides once each.
+
+def _row_tensor(t, types, name, dev=None):
+    """(dtype code, rows, columns, leading dimension, device) of a row-major GPU tensor
+    [N][C] or [C] whose rows may be apart (last dimension contiguous)."""
+    try:
+        code, at, shape = types[t.dtype], t.get_device(), t.shape
+    except (AttributeError, KeyError):
+        _refuse(t, types, name, dev)
+    if at < 0 or (dev is not None and at != dev):
+        _refuse(t, types, name, dev)
     if len(shape) == 2:
         n, c = shape
-        st = t.stride()
-        ld = st[0] if n > 1 else c
-        if (c > 1 and st[1] != 1) or ld < c:
+        ld, step = t.stride()
+        if n <= 1:
+            ld = c
+        if (step != 1 and c > 1) or ld < c:
             raise ValueError(f"{name} must be row-major with contiguous, distinct rows")
-        return code, n, c, ld
+        return code, n, c, ld, at
     if len(shape) == 1 and (shape[0] <= 1 or t.stride(0) == 1):
-        return code, 1, shape[0], shape[0]
+        return code, 1, shape[0], shape[0], at
     raise ValueError(f"{name} must be a row-major [N][C] or a contiguous [C] tensor")
 
 
 def _flat(t, types, n, name, dev):
     """dtype code of a contiguous GPU tensor of at least n elements."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda):
-        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    code = types.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name} must be one of {[str(d) for d in types]}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on another device")
+    try:
+        code = types[t.dtype]
+        if t.get_device() != dev:
+            _refuse(t, types, name, dev)
+    except (AttributeError, KeyError):
+        _refuse(t, types, name, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if t.numel() < n:
@@ -657,21 +667,26 @@ _INT32 = {torch.int32: 0}
 _FP32 = {torch.float32: F32}
 
 
+_current_device = torch.cuda.current_device
+if hasattr(torch._C, "_cuda_getDevice"):     # the same without the lazy-initialisation check
+    _current_device = torch._C._cuda_getDevice
+
+
 def _launch(dev, stream, what, fn, *args):
     """One library call on `stream` (None: the current stream of device `dev`), with that
     device current."""
-    if stream is not None:
+    if stream is None:
+        handle = _raw_current(dev) if _raw_current is not None else _current_stream_handle(dev)
+    else:
         if stream.device.index != dev:
             raise ValueError("the stream belongs to another device than the tensors")
         handle = stream.cuda_stream
-    else:
-        handle = _current_stream_handle(dev)
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
             status = fn(*args, handle)
-    if status != OK:
+    if status:
         raise SeedmmError(status, what)
 
 
@@ -696,8 +711,7 @@ def q4_gemv(mat: dict, x: torch.Tensor, M: int, K: int, group: int = 64, x_scale
     "scales", "biases": fp32 or bf16 [M*K/group]}; x fp32, bf16 or int8 [N][K] (or [K]),
     int8 rows with x_scale fp32 [N]; y [N][M] (or [M]) fp32 or bf16.  workspace: a GPU tensor
     of q4_workspace_bytes(...) bytes, allocated here if it is needed and not given."""
-    xd, N, cols, ldx = _row_tensor(x, _ROWS, "x")
-    dev = x.get_device()
+    xd, N, cols, ldx, dev = _row_tensor(x, _ROWS, "x")
     if cols < K:
         raise ValueError(f"x rows hold {cols} elements, K = {K}")
     sd = _check_q4(mat, M, K, group, dev)
@@ -708,7 +722,7 @@ def q4_gemv(mat: dict, x: torch.Tensor, M: int, K: int, group: int = 64, x_scale
     if y is None:
         with _on(stream):
             y = torch.empty((N, M) if x.dim() == 2 else (M,), dtype=y_dtype, device=x.device)
-    yd, yn, yc, ldy = _row_tensor(y, _FLOATS, "y", dev)
+    yd, yn, yc, ldy, _ = _row_tensor(y, _FLOATS, "y", dev)
     if yn < N or yc < M:
         raise ValueError(f"y must hold [{N}][{M}]")
     ws = nws = None
@@ -735,22 +749,23 @@ def add_norm(x: torch.Tensor, weight=None, delta=None, eps: float = 1e-6,
     bf16 [H] or None; out of out_dtype (float32, bfloat16, or int8 with scale fp32 [N]; scale
     is None otherwise).  residual: r in x's type (pass x itself to update it in place); x if
     there is no delta and none is asked for."""
-    xd, N, H, ldx = _row_tensor(x, _FLOATS, "x")
-    dev = x.get_device()
+    xd, N, H, ldx, dev = _row_tensor(x, _FLOATS, "x")
     dd, ldd, wd, ldr = F32, H, F32, H
     if delta is not None:
-        dd, dn, dc, ldd = _row_tensor(delta, _FLOATS, "delta", dev)
+        dd, dn, dc, ldd, _ = _row_tensor(delta, _FLOATS, "delta", dev)
         if dn != N or dc != H:
             raise ValueError("delta must have x's shape")
     if weight is not None:
         wd = _flat(weight, _FLOATS, H, "weight", dev)
-    with _on(stream):
-        if out is None:
+    if out is None:
+        with _on(stream):
             out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
-        od, on, oc, ldo = _row_tensor(out, _ROWS, "out", dev)
-        if od == I8 and scale is None:
+    od, on, oc, ldo, _ = _row_tensor(out, _ROWS, "out", dev)
+    if od == I8 and scale is None:
+        with _on(stream):
             scale = torch.empty(N, dtype=torch.float32, device=x.device)
-        if delta is not None and residual is None:
+    if delta is not None and residual is None:
+        with _on(stream):
             residual = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     if on != N or oc != H:
         raise ValueError("out must have x's shape")
@@ -759,7 +774,7 @@ def add_norm(x: torch.Tensor, weight=None, delta=None, eps: float = 1e-6,
     elif scale is not None:
         raise ValueError("scale goes with an int8 out")
     if residual is not None:
-        rd, rn, rc, ldr = _row_tensor(residual, _FLOATS, "residual", dev)
+        rd, rn, rc, ldr, _ = _row_tensor(residual, _FLOATS, "residual", dev)
         if rd != xd or rn != N or rc != H:
             raise ValueError("residual must have x's shape and type")
     _launch(dev, stream, "seedmm_add_norm", _lib.seedmm_add_norm, x.data_ptr(), xd, ldx,
@@ -778,10 +793,9 @@ def route(logits: torch.Tensor, top_k: int, bias=None, score: str = "softmax", i
     """(ids int32 [T][top_k], w fp32 [T][top_k]) of router logits fp32 or bf16 [T][E]
     (seedmm_route): the routing that moe() takes.  score "softmax", or "sigmoid" with an
     optional fp32 selection bias [E]."""
+    ld_, T, E, ldl, dev = _row_tensor(logits, _FLOATS, "logits")
     if logits.dim() != 2:
         raise ValueError("logits must be [T][E]")
-    ld_, T, E, ldl = _row_tensor(logits, _FLOATS, "logits")
-    dev = logits.get_device()
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}")
     if bias is not None:
