@@ -608,96 +608,61 @@ class ExpertCache:
 
 
 # ---- dense operators around the routed layer -----------------------------------------
+# Their arguments are checked and marshalled in the module _binding (csrc/binding.cpp).
+
+if not os.path.exists(os.path.join(_HERE, "_binding.so")):
+    raise ImportError(f"{os.path.join(_HERE, '_binding.so')} is missing: build it with "
+                      "`python -m pseudo_random_weight_amd.build`")
+from . import _binding  # noqa: E402
+
+_binding.init(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value
+                for n in ("seedmm_q4_gemv", "seedmm_q4_workspace_bytes", "seedmm_add_norm",
+                          "seedmm_route")), SeedmmError)
 
 _FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
 _ROWS = {torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8}
-
-
-def _refuse(t, types, name, dev):
-    """Why a tensor was not taken: not on a GPU, of another type, or on another device."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda):
-        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    if t.dtype not in types:
-        raise TypeError(f"{name} must be one of {[str(d) for d in types]}, got {t.dtype}")
-    raise ValueError(f"{name} is on another device")
-
-
-# The checks run on every call of a decode step, so they ask a tensor for as little as they
-# can: device, type, shape and strides once each.
-
-def _row_tensor(t, types, name, dev=None):
-    """(dtype code, rows, columns, leading dimension, device) of a row-major GPU tensor
-    [N][C] or [C] whose rows may be apart (last dimension contiguous)."""
-    try:
-        code, at, shape = types[t.dtype], t.get_device(), t.shape
-    except (AttributeError, KeyError):
-        _refuse(t, types, name, dev)
-    if at < 0 or (dev is not None and at != dev):
-        _refuse(t, types, name, dev)
-    if len(shape) == 2:
-        n, c = shape
-        ld, step = t.stride()
-        if n <= 1:
-            ld = c
-        if (step != 1 and c > 1) or ld < c:
-            raise ValueError(f"{name} must be row-major with contiguous, distinct rows")
-        return code, n, c, ld, at
-    if len(shape) == 1 and (shape[0] <= 1 or t.stride(0) == 1):
-        return code, 1, shape[0], shape[0], at
-    raise ValueError(f"{name} must be a row-major [N][C] or a contiguous [C] tensor")
-
-
-def _flat(t, types, n, name, dev):
-    """dtype code of a contiguous GPU tensor of at least n elements."""
-    try:
-        code = types[t.dtype]
-        if t.get_device() != dev:
-            _refuse(t, types, name, dev)
-    except (AttributeError, KeyError):
-        _refuse(t, types, name, dev)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if t.numel() < n:
-        raise ValueError(f"{name} has {t.numel()} elements, {n} needed")
-    return code
-
-
-_U32 = {torch.uint32: 0}
 _INT32 = {torch.int32: 0}
 _FP32 = {torch.float32: F32}
 
 
-_current_device = torch.cuda.current_device
-if hasattr(torch._C, "_cuda_getDevice"):     # the same without the lazy-initialisation check
-    _current_device = torch._C._cuda_getDevice
-
-
-def _launch(dev, stream, what, fn, *args):
-    """One library call on `stream` (None: the current stream of device `dev`), with that
-    device current."""
-    if stream is None:
-        handle = _raw_current(dev) if _raw_current is not None else _current_stream_handle(dev)
-    else:
-        if stream.device.index != dev:
-            raise ValueError("the stream belongs to another device than the tensors")
-        handle = stream.cuda_stream
-    if dev == _current_device():
-        status = fn(*args, handle)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, handle)
-    if status:
-        raise SeedmmError(status, what)
+def _flat(t, types, n, name, dev):
+    """dtype code of a contiguous GPU tensor of at least n elements."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype not in types:
+        raise TypeError(f"{name} must be one of {[str(d) for d in types]}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() < n:
+        raise ValueError(f"{name} has {t.numel()} elements, {n} needed")
+    return types[t.dtype]
 
 
 def _check_q4(mat, M, K, group, dev):
     if group not in (32, 64, 128) or K % group:
         raise ValueError(f"K = {K} must be a multiple of the group, and the group 32, 64 or 128")
-    _flat(mat["weight"], _U32, M * (K // 8), "weight", dev)
+    _flat(mat["weight"], {torch.uint32: 0}, M * (K // 8), "weight", dev)
     sd = _flat(mat["scales"], _FLOATS, M * (K // group), "scales", dev)
     if _flat(mat["biases"], _FLOATS, M * (K // group), "biases", dev) != sd:
         raise TypeError("scales and biases must have one type")
     return sd
+
+
+def _handle(stream, t):
+    """A stream's handle for the call on tensor t's device (None: its current stream)."""
+    if stream is None:
+        return None
+    if stream.device.index != t.get_device():
+        raise ValueError("the stream belongs to another device than the tensors")
+    return stream.cuda_stream
+
+
+def _gpu(t, name):
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    return t
 
 
 def q4_workspace_bytes(x_dtype, group: int, M: int, K: int, N: int) -> int:
@@ -711,34 +676,19 @@ def q4_gemv(mat: dict, x: torch.Tensor, M: int, K: int, group: int = 64, x_scale
     "scales", "biases": fp32 or bf16 [M*K/group]}; x fp32, bf16 or int8 [N][K] (or [K]),
     int8 rows with x_scale fp32 [N]; y [N][M] (or [M]) fp32 or bf16.  workspace: a GPU tensor
     of q4_workspace_bytes(...) bytes, allocated here if it is needed and not given."""
-    xd, N, cols, ldx, dev = _row_tensor(x, _ROWS, "x")
-    if cols < K:
-        raise ValueError(f"x rows hold {cols} elements, K = {K}")
-    sd = _check_q4(mat, M, K, group, dev)
-    if xd == I8:
-        _flat(x_scale, _FP32, N, "x_scale", dev)
-    elif x_scale is not None:
-        raise ValueError("x_scale goes with int8 activations")
     if y is None:
         with _on(stream):
-            y = torch.empty((N, M) if x.dim() == 2 else (M,), dtype=y_dtype, device=x.device)
-    yd, yn, yc, ldy, _ = _row_tensor(y, _FLOATS, "y", dev)
-    if yn < N or yc < M:
-        raise ValueError(f"y must hold [{N}][{M}]")
-    ws = nws = None
-    if workspace is None and N > 5:
-        need = q4_workspace_bytes(x.dtype, group, M, K, N)
-        if need:
-            with _on(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    if workspace is not None:
-        if workspace.get_device() != dev or not workspace.is_contiguous():
-            raise ValueError("the workspace must be a contiguous tensor on x's device")
-        ws, nws = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _launch(dev, stream, "seedmm_q4_gemv", _lib.seedmm_q4_gemv, mat["weight"].data_ptr(),
-            mat["scales"].data_ptr(), mat["biases"].data_ptr(), sd, group, x.data_ptr(), xd, ldx,
-            None if x_scale is None else x_scale.data_ptr(), y.data_ptr(), yd, ldy, M, K, N,
-            ws, nws or 0)
+            y = torch.empty((*_gpu(x, "x").shape[:-1], M), dtype=y_dtype, device=x.device)
+    if stream is not None:
+        _gpu(x, "x")
+        if workspace is None and x.dtype in _ROWS and x.dim() == 2:
+            need = q4_workspace_bytes(x.dtype, group, M, K, x.shape[0])
+            if need:       # scratch of a call on another stream belongs to that stream
+                with _on(stream):
+                    workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        stream = _handle(stream, x)
+    _binding.q4_gemv(mat["weight"], mat["scales"], mat["biases"], group, x, x_scale, y, workspace,
+                     M, K, stream)
     return y
 
 
@@ -749,39 +699,18 @@ def add_norm(x: torch.Tensor, weight=None, delta=None, eps: float = 1e-6,
     bf16 [H] or None; out of out_dtype (float32, bfloat16, or int8 with scale fp32 [N]; scale
     is None otherwise).  residual: r in x's type (pass x itself to update it in place); x if
     there is no delta and none is asked for."""
-    xd, N, H, ldx, dev = _row_tensor(x, _FLOATS, "x")
-    dd, ldd, wd, ldr = F32, H, F32, H
-    if delta is not None:
-        dd, dn, dc, ldd, _ = _row_tensor(delta, _FLOATS, "delta", dev)
-        if dn != N or dc != H:
-            raise ValueError("delta must have x's shape")
-    if weight is not None:
-        wd = _flat(weight, _FLOATS, H, "weight", dev)
     if out is None:
         with _on(stream):
-            out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
-    od, on, oc, ldo, _ = _row_tensor(out, _ROWS, "out", dev)
-    if od == I8 and scale is None:
+            out = torch.empty(_gpu(x, "x").shape, dtype=out_dtype, device=x.device)
+    if scale is None and out.dtype is torch.int8:
         with _on(stream):
-            scale = torch.empty(N, dtype=torch.float32, device=x.device)
+            scale = torch.empty(_gpu(x, "x").shape[:-1] if x.dim() > 1 else 1, dtype=torch.float32,
+                                device=x.device)
     if delta is not None and residual is None:
         with _on(stream):
-            residual = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if on != N or oc != H:
-        raise ValueError("out must have x's shape")
-    if od == I8:
-        _flat(scale, _FP32, N, "scale", dev)
-    elif scale is not None:
-        raise ValueError("scale goes with an int8 out")
-    if residual is not None:
-        rd, rn, rc, ldr, _ = _row_tensor(residual, _FLOATS, "residual", dev)
-        if rd != xd or rn != N or rc != H:
-            raise ValueError("residual must have x's shape and type")
-    _launch(dev, stream, "seedmm_add_norm", _lib.seedmm_add_norm, x.data_ptr(), xd, ldx,
-            None if delta is None else delta.data_ptr(), dd, ldd,
-            None if weight is None else weight.data_ptr(), wd, eps,
-            None if residual is None else residual.data_ptr(), ldr, out.data_ptr(), od, ldo,
-            None if scale is None else scale.data_ptr(), N, H)
+            residual = torch.empty(_gpu(x, "x").shape, dtype=x.dtype, device=x.device)
+    _binding.add_norm(x, weight, delta, eps, residual, out, scale,
+                      None if stream is None else _handle(stream, _gpu(x, "x")))
     return out, scale, x if residual is None else residual
 
 
@@ -793,26 +722,20 @@ def route(logits: torch.Tensor, top_k: int, bias=None, score: str = "softmax", i
     """(ids int32 [T][top_k], w fp32 [T][top_k]) of router logits fp32 or bf16 [T][E]
     (seedmm_route): the routing that moe() takes.  score "softmax", or "sigmoid" with an
     optional fp32 selection bias [E]."""
-    ld_, T, E, ldl, dev = _row_tensor(logits, _FLOATS, "logits")
-    if logits.dim() != 2:
-        raise ValueError("logits must be [T][E]")
-    if score not in _SCORES:
+    kind = _SCORES.get(score)
+    if kind is None:
         raise ValueError(f"score must be one of {sorted(_SCORES)}")
-    if bias is not None:
-        _flat(bias, _FP32, E, "bias", dev)
-    if not 1 <= top_k <= min(E, 64):
-        raise ValueError(f"top_k = {top_k} must be in [1, min(E, 64)], E = {E}")
     if ids is None or w is None:
+        if _gpu(logits, "logits").dim() != 2 or top_k < 1:
+            raise ValueError("logits must be [T][E] and top_k positive")
+        shape = (logits.shape[0], top_k)
         with _on(stream):
             if ids is None:
-                ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+                ids = torch.empty(shape, dtype=torch.int32, device=logits.device)
             if w is None:
-                w = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
-    _flat(ids, _INT32, T * top_k, "ids", dev)
-    _flat(w, _FP32, T * top_k, "w", dev)
-    _launch(dev, stream, "seedmm_route", _lib.seedmm_route, logits.data_ptr(), ld_, ldl,
-            None if bias is None else bias.data_ptr(), _SCORES[score], T, E, top_k, ids.data_ptr(),
-            w.data_ptr())
+                w = torch.empty(shape, dtype=torch.float32, device=logits.device)
+    _binding.route(logits, top_k, bias, kind, ids, w,
+                   None if stream is None else _handle(stream, _gpu(logits, "logits")))
     return ids, w
 
 
@@ -875,10 +798,10 @@ class MoeBlock:
             raise ValueError("the workspace is on another device")
         sd = None if side is None else ctypes.byref(side.c())
         ptr = lambda t: None if t is None else t.data_ptr()
-
-        def call(*a):
-            return _lib.seedmm_moe_block(*a, sd)
-        _launch(dev, stream, "seedmm_moe_block", call, ctypes.byref(self._c), r.data_ptr(), rd,
-                ptr(delta), dd, y.data_ptr(), ptr(ids), ptr(w), T, workspace.data_ptr(),
-                workspace.numel() * workspace.element_size())
+        handle = _handle(stream, r)
+        with torch.cuda.device(dev):
+            _check(_lib.seedmm_moe_block(
+                ctypes.byref(self._c), r.data_ptr(), rd, ptr(delta), dd, y.data_ptr(), ptr(ids),
+                ptr(w), T, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                _current_stream_handle(dev) if handle is None else handle, sd), "seedmm_moe_block")
         return y

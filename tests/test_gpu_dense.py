@@ -506,8 +506,21 @@ def test_binding_refusals_on_gpu_tensors(sm):
     assert e.value.status == sm.EALIGN
     with pytest.raises(ValueError, match="delta"):
         sm.add_norm(x, delta=x[:1])
-    with pytest.raises(ValueError, match="distinct rows"):
-        sm.add_norm(x, delta=x[:1].expand(2, 64))
+    for bad in (x[:1].expand(2, 64), torch.zeros(64, 2, dtype=torch.bfloat16, device="cuda").t(),
+                torch.zeros(2, 128, dtype=torch.bfloat16, device="cuda")[:, ::2]):
+        with pytest.raises(ValueError, match="distinct rows"):
+            sm.add_norm(x, delta=bad)
+    with pytest.raises(ValueError, match="row-major"):
+        sm.add_norm(x, delta=x[None], residual=x)
+    with pytest.raises(ValueError, match="workspace"):
+        sm.q4_gemv(mat, x, 16, 64, workspace=torch.zeros(64))
+    with pytest.raises(sm.SeedmmError) as e:
+        sm.q4_gemv(mat, x.repeat(20, 1), 16, 64, workspace=torch.zeros(64, device="cuda"))
+    assert e.value.status == sm.EWORKSPACE
+    with pytest.raises(ValueError, match="T..E"):
+        sm.route(torch.zeros(8, device="cuda"), 2)
+    with pytest.raises(TypeError, match="logits must be one of"):
+        sm.route(torch.zeros(2, 8, dtype=torch.float64, device="cuda"), 2)
     with pytest.raises(ValueError, match="residual"):
         sm.add_norm(x, delta=x, residual=torch.empty(2, 64, device="cuda"))
     with pytest.raises(ValueError, match="int8"):
