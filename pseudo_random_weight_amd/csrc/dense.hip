@@ -1066,6 +1066,7 @@ __device__ __forceinline__ float sigmoid32(float l) {
 template <int NPL, bool SIG, int LT>
 __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
     __shared__ int cand[4][64];
+    __shared__ float candl[4][64], candb[SIG ? 4 : 1][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t t = (int64_t)blockIdx.x * 4 + wave;
@@ -1077,21 +1078,42 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
         l[i] = e < a.E ? load_el(a.lg, LT, t * a.ldl + e) : 0.f;
         if constexpr (SIG) bias[i] = e < a.E && a.bias ? a.bias[e] : 0.f;
     }
-    uint32_t key[NPL], top[1] = {0};
+    uint32_t key[NPL], top = 0;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         float v = l[i];
         if constexpr (SIG) v = sigmoid32(l[i]) + bias[i];
         key[i] = i * 64 + lane >= a.E ? 0u : l[i] > -INFINITY && v > -INFINITY ? key32(v) : 1u;
-        top[0] = max(top[0], key[i]);
+        top = max(top, key[i]);
     }
+    // the bound's bits from the top: the largest number that top_k lane maxima reach, or the
+    // first that exactly top_k reach (the scalar unit counts; the vector units compare once)
     uint32_t bound = 0;
-    for (int s = 0; s < a.k; ++s) {
-        int e;
-        bound = largest<1>(top, lane, e);
-        clear_key<1>(top, lane, e);
+    for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
+        const int c = __popcll(__ballot(top >= (bound | bit)));
+        if (c >= a.k) bound |= bit;
+        if (c == a.k) break;
     }
-    const bool all = bound <= 1;      // fewer than top_k lanes with an eligible expert
+    const bool all = __popcll(__ballot(top > 1)) < a.k;      // too few lanes with an eligible expert
+    // where lanes hold many experts more than 64 can reach it: raise it between bounds
+    if constexpr (NPL >= 8) {
+        auto reach = [&](uint32_t b) {
+            int c = 0;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) c += __popcll(__ballot(key[i] >= b));
+            return c;
+        };
+        if (!all && reach(bound) > 64) {
+            uint32_t lo = bound, hi = 0xFFFFFFFFu;     // more than 64 reach lo
+            while (lo < hi) {
+                const uint32_t mid = lo + (hi - lo) / 2 + 1;
+                const int c = reach(mid);
+                if (c > 64) lo = mid;
+                else if (c < a.k) hi = mid - 1;
+                else { bound = mid; break; }
+            }
+        }
+    }
     // fp32 scores are off by less than 2^-22 + 2^-24 |score|, two of them by twice that
     if constexpr (SIG) {
         const float b = unkey32(bound), low = b - 9.5367431640625e-7f * (1.0f + fabsf(b));
@@ -1103,22 +1125,31 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
         const bool near = key[i] > 1 && key[i] >= bound;
         const uint64_t m = __ballot(near);
         const int at = count + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
-        if (near && at < 64) cand[wave][at] = i * 64 + lane;
+        if (near && at < 64) {
+            cand[wave][at] = i * 64 + lane;
+            candl[wave][at] = l[i];
+            if constexpr (SIG) candb[wave][at] = bias[i];
+        }
         count += __popcll(m);
     }
 
     int mine = 0, slot = -1;          // this lane's expert and its slot
     float ml = -INFINITY;             // its logit, -inf if it is masked
+    double p = 0.0;                   // its sigmoid
     if (!all && count <= 64) {
         wave_order();
         if (lane < count) {
             mine = cand[wave][lane];
-            ml = load_el(a.lg, LT, t * a.ldl + mine);
+            ml = candl[wave][lane];
         }
         uint64_t k64 = 0;
         if (lane < count) {
-            if constexpr (SIG) k64 = key64(sigmoid64(ml) + (a.bias ? (double)a.bias[mine] : 0.0));
-            else k64 = key32(ml);
+            if constexpr (SIG) {
+                p = sigmoid64(ml);
+                k64 = key64(p + (double)candb[wave][lane]);
+            } else {
+                k64 = key32(ml);
+            }
         }
         int rank = 0;
         for (int c = 0; c < count; ++c) {   // candidates are in the experts' order
@@ -1138,7 +1169,10 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
             clear_key<NPL>(k64, lane, e);
             if (lane == s) { mine = e; slot = s; ml = best > 1 ? 0.f : -INFINITY; }
         }
-        if (slot >= 0 && ml == 0.f) ml = load_el(a.lg, LT, t * a.ldl + mine);
+        if (slot >= 0 && ml == 0.f) {
+            ml = load_el(a.lg, LT, t * a.ldl + mine);
+            p = sigmoid64(ml);
+        }
     } else {
         for (int s = 0; s < a.k; ++s) {
             int e;
@@ -1151,7 +1185,7 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
     const bool weighs = slot >= 0 && ml > -INFINITY;
     float w;
     if constexpr (SIG) {
-        w = (float)sigmoid64(ml);
+        w = (float)p;
     } else {
         const float m = wave_max(weighs ? ml : -INFINITY);
         w = ml == m ? 1.0f : expf(ml - m);
