@@ -61,6 +61,14 @@ __device__ __forceinline__ void transpose_quarters(uint32_t (&w)[4]) {
     w[0] = c[0]; w[1] = c[1]; w[2] = d[0]; w[3] = d[1];
 }
 
+// A table of 16-byte pieces in LDS with C of them a row, read by 16 lanes at a time from 16
+// rows: the place of row `row`'s piece c, permuted so that the 16 lie in different banks
+// (64 banks = 16 pieces, so 16 / C rows share a stretch of banks).
+template <int C>
+__device__ __forceinline__ int piece(int row, int c) {
+    return row * C + (c ^ (row / (16 / C) & (C - 1)));
+}
+
 // LDS accesses of one wave keep their order across this point (they run in order; the
 // compiler must not exchange them).
 __device__ __forceinline__ void wave_order() {
@@ -318,11 +326,11 @@ __global__ __launch_bounds__(kQ4Waves * 64) void k_q4(const Q4Args a, int slab) 
 #pragma unroll
             for (int i = 0; i < SS; ++i) {
                 const int lr = 16 / SS * i + lsub;
-                bw[lr * CR + (lcol ^ (lr & (CR - 1)))] = w[i];
+                bw[piece<CR>(lr, lcol)] = w[i];
             }
             wave_order();
 #pragma unroll
-            for (int j = 0; j < SS; ++j) v[j] = bw[r * CR + ((4 * j + q) ^ (r & (CR - 1)))];
+            for (int j = 0; j < SS; ++j) v[j] = bw[piece<CR>(r, 4 * j + q)];
             wave_order();
             if (c0 + KW * SC < kn) load(c0 + KW * SC);
 #pragma unroll
@@ -461,20 +469,20 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OC
     const int G = a.K / GROUP;
 
     // Slabs of SP steps (64 columns each).  Piece u of a step = 16 bytes `u & 7` of tile row
-    // u >> 3, kept at slot (u & 7) ^ (row & 7); the codes likewise, CW pieces a row.
+    // u >> 3; the codes likewise, CW pieces a row.
     int64_t src[NST], wsrc[NWT];
     int dst[NST], wdst[NWT];
 #pragma unroll
     for (int i = 0; i < NST; ++i) {
         const int u = i * NTH + tid, row = u >> 3, p = row / BT, t = row % BT;
         src[i] = ((int64_t)p * a.N + min(n0 + t, a.N - 1)) * c.Kp + 8 * (u & 7);
-        dst[i] = row * 8 + ((u & 7) ^ (row & 7));
+        dst[i] = piece<8>(row, u & 7);
     }
 #pragma unroll
     for (int i = 0; i < NWT; ++i) {
         const int u = i * NTH + tid, row = u / CW;
         wsrc[i] = (mb + row < a.M ? mb + row : a.M - 1) * (a.K / 8);
-        wdst[i] = row * CW + ((u % CW) ^ (row & (CW - 1)));
+        wdst[i] = piece<CW>(row, u % CW);
     }
     int64_t row[MT];
 #pragma unroll
@@ -581,7 +589,7 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OC
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const int wr = 32 * (MT * wm + mt) + r;
-            const u32x4 wv = ws[wr * CW + ((2 * b + h) ^ (wr & (CW - 1)))];
+            const u32x4 wv = ws[piece<CW>(wr, 2 * b + h)];
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[mt][j] = wv[j];
 #pragma unroll
@@ -598,7 +606,7 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OC
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int ch = GROUP == 32 ? 4 * (j >> 1) + 2 * h + (j & 1) : 4 * h + j;
-                        xa[p][j] = __builtin_bit_cast(bf16x8, xs[b][(p * BT + t) * 8 + (ch ^ (t & 7))]);
+                        xa[p][j] = __builtin_bit_cast(bf16x8, xs[b][piece<8>(p * BT + t, ch)]);
                     }
             }
             if (tt == 0) {
