@@ -667,3 +667,98 @@ def test_block_mixed_pack(sm):
     torch.cuda.synchronize()
     assert same is r and bool((y == ref).all())
     assert blk.moe(r[:0]).shape == (0, H)
+
+
+def test_captured_operators_replay_like_eager(sm):
+    """q4_gemv (few tokens, many tokens, K split), add_norm and route captured with buffers of
+    the caller's, replayed with eager work of their own in between: every replay's bits are
+    the eager call's on the inputs of the moment."""
+    import torch
+    for (N, M, K, xt) in [(1, 100, 2048, "bf16"), (16, 70, 512, "f32"), (40, 300, 4096, "bf16"),
+                          (600, 260, 320, "i8")]:
+        say("captured", N, M, K, xt)
+        w, sc, bi, xv, xs = q4_case(N, M, K, 64, xt, "bf16", 31)
+        mat, x, xsd = to_mat(w, sc, bi), xv.cuda(), None if xs is None else xs.cuda()
+        y = torch.empty(N, M, device="cuda")
+        nb = sm.q4_workspace_bytes(DT[xt], 64, M, K, N)
+        ws = torch.empty(max(nb, 16), dtype=torch.uint8, device="cuda")
+        hid = torch.randn(N, M, device="cuda")
+        out, res = torch.empty(N, M, dtype=torch.int8, device="cuda"), torch.empty(N, M, device="cuda")
+        scale = torch.empty(N, device="cuda")
+        k = min(8, M)
+        ids, wt = torch.empty(N, k, dtype=torch.int32, device="cuda"), torch.empty(N, k, device="cuda")
+
+        def step():
+            sm.q4_gemv(mat, x, M, K, 64, x_scale=xsd, y=y, workspace=ws)
+            sm.add_norm(hid, delta=y, out=out, scale=scale, residual=res)
+            sm.route(y, k, ids=ids, w=wt)
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        for r in range(4):
+            _, _, _, nx, _ = q4_case(N, M, K, 64, xt, "bf16", 40 + r)
+            x.copy_(nx.cuda())
+            ye = sm.q4_gemv(mat, x, M, K, 64, x_scale=xsd)          # its own workspace
+            oe, se, re = sm.add_norm(hid, delta=ye, out_dtype=torch.int8)
+            ie, we = sm.route(ye, k)
+            ws.fill_(255)
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            for a, b in ((y, ye), (out, oe), (scale, se), (res, re), (ids, ie), (wt, we)):
+                assert bool((a == b).all())
+
+
+def test_concurrent_threads_and_streams(sm):
+    """Four host threads at once, each with its own stream and workspace: every product, norm
+    and choice equals the single-thread call bit for bit."""
+    import threading
+
+    import torch
+    cases = []
+    for i, (N, M, K, xt) in enumerate([(1, 500, 2048, "bf16"), (33, 200, 1024, "i8"),
+                                       (300, 257, 640, "bf16"), (9, 300, 512, "f32")]):
+        w, sc, bi, xv, xs = q4_case(N, M, K, 64, xt, "bf16", 50 + i)
+        mat, x, xsd = to_mat(w, sc, bi), xv.cuda(), None if xs is None else xs.cuda()
+        y = sm.q4_gemv(mat, x, M, K, 64, x_scale=xsd)
+        cases.append((mat, x, xsd, M, K, y, sm.add_norm(y, out_dtype=torch.int8)[:2], sm.route(y, 8)))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        mat, x, xsd, M, K, y, (o, s), (ids, wt) = cases[i]
+        st = torch.cuda.Stream()
+        try:
+            for _ in range(16):
+                y2 = sm.q4_gemv(mat, x, M, K, 64, x_scale=xsd, stream=st)
+                o2, s2, _ = sm.add_norm(y2, out_dtype=torch.int8, stream=st)
+                i2, w2 = sm.route(y2, 8, stream=st)
+                st.synchronize()
+                if not all(bool((a == b).all()) for a, b in ((y, y2), (o, o2), (s, s2), (ids, i2), (wt, w2))):
+                    bad.append(i)
+        except Exception as e:    # reported by the assertion below
+            bad.append((i, repr(e)))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
+
+
+def test_router_with_many_experts_near_the_choice(sm):
+    """Scores so close that fp32 cannot order them (sigmoids of logits a unit apart in the
+    last place, and all beyond 20 where they differ by less than 2^-24), in numbers below
+    and above the 64 that are compared at once."""
+    import torch
+    for E in (40, 90, 300, 1000):
+        for k in (1, 8, 33):
+            base = torch.full((3, E), 0.25)
+            step = torch.arange(E).flip(0).float() * 2.0 ** -24
+            lg = torch.stack([base[0] + step * 2, 20 + step * 2.0 ** 5, base[2]])
+            lg[2, ::3] = lg[2, ::3] + 2.0 ** -25
+            check_route(sm, lg, min(k, E), "sigmoid")
+            check_route(sm, lg, min(k, E), "sigmoid", (torch.arange(E) % 5).float() * 2.0 ** -20)
+            check_route(sm, lg, min(k, E), "softmax")
