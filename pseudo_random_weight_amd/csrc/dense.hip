@@ -193,6 +193,24 @@ __device__ __forceinline__ float place8(const Raw8<XT>& x, char* dst, int64_t ro
     return sum;
 }
 
+// the same for 8-bit rows as bf16 (exact)
+__device__ __forceinline__ float place8_as_bf16(const Raw8<SEEDMM_I8>& x, char* dst) {
+    float f[8], sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        f[i] = (float)(int8_t)(x.u[i >> 2] >> 8 * (i & 3));
+        sum += f[i];
+    }
+    u32x4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int e = i < 2 ? 4 * i : 4 * i - 7;
+        o[i] = (__float_as_uint(f[e]) >> 16) | (__float_as_uint(f[e + 2]) & 0xFFFF0000u);
+    }
+    *(u32x4*)dst = o;
+    return sum;
+}
+
 // A few tokens.  A wave takes 16 weight rows; KW waves of a workgroup share a row tile and
 // take its slabs of 256 columns in turn, each loaded while the one before is multiplied,
 // the first before the activations are staged.  8 lanes load the 128 bytes of a row, whole
@@ -403,21 +421,7 @@ __global__ __launch_bounds__(256) void k_q4_rows(const Q4Args a, uint16_t* xp, u
         float sum = 0.f;
         if (in) {
             if constexpr (XT == SEEDMM_I8) {
-                u32x2 v = {0u, 0u};
-                if (ok) v = *(const u32x2*)((const int8_t*)a.x + n * a.ldx + kk);
-                float f[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    f[i] = (float)(int8_t)(v[i >> 2] >> 8 * (i & 3));
-                    sum += f[i];
-                }
-                u32x4 o;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int e = i < 2 ? 4 * i : 4 * i - 7;
-                    o[i] = (__float_as_uint(f[e]) >> 16) | (__float_as_uint(f[e + 2]) & 0xFFFF0000u);
-                }
-                *(u32x4*)(xp + n * Kp + kk) = o;
+                sum = place8_as_bf16(load8<XT>(a.x, n * a.ldx + kk, ok), (char*)(xp + n * Kp + kk));
             } else {
                 sum = place8<XT>(load8<XT>(a.x, n * a.ldx + kk, ok), (char*)(xp + n * Kp + kk), plane * 2);
             }
@@ -441,7 +445,10 @@ __global__ __launch_bounds__(256) void k_q4_rows(const Q4Args a, uint16_t* xp, u
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-template <int PL, bool SF32, int GROUP, int TT, int MT, int WN, int WM, int SP, int OCC>
+// RAW: the type of activation rows taken as they are (-1: laid out by k_q4_rows).  They are
+// put in the operands' order on their way to LDS, where the groups' sums go as well; the
+// bias term is then one more fma an element and group.
+template <int RAW, int PL, bool SF32, int GROUP, int TT, int MT, int WN, int WM, int SP, int OCC>
 __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OCC))) void k_q4_wide(const Q4Wide c) {
     constexpr int BT = 32 * TT * WN, BM = 32 * MT * WM, NTH = 64 * WN * WM;
     constexpr int NST = PL * BT * 8 / NTH;      // 16-byte pieces of a step a thread stages
@@ -450,6 +457,11 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OC
     static_assert(PL * BT * 8 % NTH == 0 && BM * CW % NTH == 0, "whole pieces");
     __shared__ u32x4 xs[SP][PL * BT * 8];
     __shared__ u32x4 ws[BM * CW];
+    constexpr bool LAID = RAW < 0;
+    static_assert(LAID || (PL == 1 && TT * MT == 1 && WN == 1), "raw rows: one tile a wave");
+    constexpr int XB = RAW == SEEDMM_I8 ? 1 : 2;          // bytes of a staged element
+    constexpr int NGB = 64 * SP / GROUP;                  // groups a slab
+    __shared__ __align__(16) float gx[LAID ? 1 : NGB][LAID ? 4 : BT];
     const Q4Args& a = c.a;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -475,7 +487,8 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OC
 #pragma unroll
     for (int i = 0; i < NST; ++i) {
         const int u = i * NTH + tid, row = u >> 3, p = row / BT, t = row % BT;
-        src[i] = ((int64_t)p * a.N + min(n0 + t, a.N - 1)) * c.Kp + 8 * (u & 7);
+        if constexpr (LAID) src[i] = ((int64_t)p * a.N + min(n0 + t, a.N - 1)) * c.Kp + 8 * (u & 7);
+        else src[i] = (int64_t)min(n0 + t, a.N - 1) * a.ldx + 8 * (u & 7);
         dst[i] = piece<8>(row, u & 7);
     }
 #pragma unroll
@@ -490,27 +503,63 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OC
     constexpr int NG = GROUP == 32 ? 2 : 1;               // groups a step
     constexpr int NGS = 64 * SP >= GROUP ? 64 * SP / GROUP : 1;
     u32x4 stage[SP][NST], wstage[NWT];
-    Scales<SF32, NGS> snext[MT];
-    // Rows of activations are zero from K to Kp.  Past K the codes of the row's last columns
-    // are loaded again, and scales are 0.
+    Scales<SF32, NGS> snext[MT], bnext[LAID ? 1 : MT];
+    // Activations are zero past K.  There the codes of the row's last columns are loaded
+    // again, and scales are 0.
     auto fetch = [&](int k) {
 #pragma unroll
         for (int b = 0; b < SP; ++b)
 #pragma unroll
-            for (int i = 0; i < NST; ++i) stage[b][i] = *(const u32x4*)(c.xp + src[i] + k + 64 * b);
+            for (int i = 0; i < NST; ++i) {
+                if constexpr (LAID) {
+                    stage[b][i] = *(const u32x4*)(c.xp + src[i] + k + 64 * b);
+                } else {
+                    const Raw8<RAW> v = load8<RAW>(a.x, src[i] + k + 64 * b, k + 64 * b + 8 * (tid & 7) < a.K);
+#pragma unroll
+                    for (int j = 0; j < 2 * XB; ++j) stage[b][i][j] = v.u[j];
+                }
+            }
 #pragma unroll
         for (int i = 0; i < NWT; ++i) {
             const int kw = k + 32 * ((i * NTH + tid) % CW);
             wstage[i] = *(const u32x4*)(a.w + wsrc[i] + (kw < a.K ? kw : a.K - 32) / 8);
         }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) snext[mt].load(a.s, row[mt] * G + k / GROUP, G - k / GROUP);
+        for (int mt = 0; mt < MT; ++mt) {
+            snext[mt].load(a.s, row[mt] * G + k / GROUP, G - k / GROUP);
+            if constexpr (!LAID) bnext[mt].load(a.b, row[mt] * G + k / GROUP, G - k / GROUP);
+        }
     };
     auto put = [&]() {
 #pragma unroll
-        for (int b = 0; b < SP; ++b)
+        for (int i = 0; i < NST; ++i) {
+            float sum[SP];
 #pragma unroll
-            for (int i = 0; i < NST; ++i) xs[b][dst[i]] = stage[b][i];
+            for (int b = 0; b < SP; ++b) {
+                if constexpr (LAID) {
+                    xs[b][dst[i]] = stage[b][i];
+                } else {
+                    Raw8<RAW> v;
+#pragma unroll
+                    for (int j = 0; j < 2 * XB; ++j) v.u[j] = stage[b][i][j];
+                    if constexpr (RAW == SEEDMM_I8) sum[b] = place8_as_bf16(v, (char*)&xs[b][dst[i]]);
+                    else sum[b] = place8<RAW>(v, (char*)&xs[b][dst[i]], 0);
+                }
+            }
+            if constexpr (!LAID) {
+                const int t = (i * NTH + tid) >> 3;
+#pragma unroll
+                for (int b = 0; b < SP; ++b) {
+                    if (GROUP == 128 && (b & 1)) continue;
+                    float v = sum[b];
+                    if constexpr (GROUP == 128) v += sum[b + 1];
+#pragma unroll
+                    for (int d = 1; d < (GROUP < 64 ? GROUP / 8 : 8); d *= 2) v += __shfl_xor(v, d);
+                    if (GROUP == 32 ? (tid & 3) == 0 : (tid & 7) == 0)
+                        gx[64 * b / GROUP + (GROUP == 32 ? (tid & 7) >> 2 : 0)][t] = v;
+                }
+            }
+        }
 #pragma unroll
         for (int i = 0; i < NWT; ++i) ws[wdst[i]] = wstage[i];
     };
@@ -523,7 +572,7 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OC
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[tt][mt][i] = 0.f;
     fetch(kb);
-    {   // bias term: the splits take 16 groups in turn
+    if constexpr (LAID) {   // bias term: the splits take 16 groups in turn
         for (int g0 = 16 * blockIdx.y; g0 < G; g0 += 16 * gridDim.y) {
             const int gl = g0 + 8 * h;
             bf16x8 bb[MT][SF32 ? 3 : 1];
@@ -580,9 +629,10 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OC
     }
     // A slab's activations, codes and scales are loaded while the one before is multiplied
     // and take its place in LDS after it.
-    Scales<SF32, NGS> sc[MT];
+    Scales<SF32, NGS> sc[MT], bc[LAID ? 1 : MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) sc[mt] = snext[mt];
+    if constexpr (!LAID) bc[0] = bnext[0];
     auto step = [&](int b) {
         uint32_t w[MT][4];
         float s[MT][NG];
@@ -641,6 +691,21 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OC
                 for (int g = 0; g < NG; ++g) d[1][g] = d[0][g];
             }
         }
+        if constexpr (!LAID) {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                if (GROUP == 128 && (b & 1)) continue;
+                const float bv = bc[0].get(64 * b / GROUP + g);
+                const float* const x = gx[64 * b / GROUP + g];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f32x4 X = *(const f32x4*)(x + 8 * q + 4 * h);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        acc[0][0][4 * q + v] = __builtin_fmaf(bv, X[v], acc[0][0][4 * q + v]);
+                }
+            }
+        }
 #pragma unroll
         for (int g = 0; g < NG; ++g) sp[g] = s[MT - 1][g];
         // spread the vector work between the instructions of a step (4096 x 8192 x 2048:
@@ -664,6 +729,7 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OC
             put();
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) sc[mt] = snext[mt];
+            if constexpr (!LAID) bc[0] = bnext[0];
             __syncthreads();
         }
     }
@@ -1243,6 +1309,7 @@ void launch_q4_jn(const Q4Args& a, hipStream_t st) {
 struct Q4Plan {
     bool wide;
     bool two;                      // tiles of 64 tokens, else of 32
+    bool laid;                     // activations laid out by a launch of their own
     int Kp, Gp, S, ksplit, tn, tm;
     size_t xg, part, total;
 };
@@ -1270,8 +1337,14 @@ Q4Plan q4_plan(int x_dtype, int group, int M, int K, int N) {
     const int per = (int)((slabs + S - 1) / S);
     p.ksplit = per * slab;
     p.S = (slabs + per - 1) / per;
-    p.xg = align_up((size_t)PL * (size_t)N * (size_t)p.Kp * 2);
-    p.part = p.xg + align_up((size_t)3 * (size_t)N * (size_t)p.Gp * 2);
+    // A launch that lays the rows out costs about 3 us; in the product it is done once a row
+    // tile (61 x 5125 x 4160, 10 million elements so: 23.0 us laid out, 20.5 not; 64 x 8192 x
+    // 8192, 34 million: 31.8 and 33.9; 4096 x 100 x 2048, 8 million: 24.0 and 17.4).
+    p.laid = p.two || (int64_t)N * K > (1 << 24) / tm;
+    if (p.laid) {
+        p.xg = align_up((size_t)PL * (size_t)N * (size_t)p.Kp * 2);
+        p.part = p.xg + align_up((size_t)3 * (size_t)N * (size_t)p.Gp * 2);
+    }
     p.total = p.part + (p.S > 1 ? align_up((size_t)p.S * (size_t)N * (size_t)M * 4) : 0);
     return p;
 }
@@ -1286,14 +1359,17 @@ void launch_q4_group(const Q4Args& a, const Q4Plan& p, void* ws, hipStream_t st)
     }
     uint16_t* xp = (uint16_t*)ws;
     uint16_t* xg = (uint16_t*)((char*)ws + p.xg);
-    const int64_t runs = (int64_t)a.N * (p.Kp / 8), blocks = (runs + 255) / 256;
-    hipLaunchKernelGGL((k_q4_rows<XT, GROUP>), dim3((unsigned)(blocks < 65536 ? blocks : 65536)),
-                       dim3(256), 0, st, a, xp, xg, p.Kp, p.Gp);
+    if (p.laid) {
+        const int64_t runs = (int64_t)a.N * (p.Kp / 8), blocks = (runs + 255) / 256;
+        hipLaunchKernelGGL((k_q4_rows<XT, GROUP>), dim3((unsigned)(blocks < 65536 ? blocks : 65536)),
+                           dim3(256), 0, st, a, xp, xg, p.Kp, p.Gp);
+    }
     Q4Wide c = {a, xp, xg, p.S > 1 ? (float*)((char*)ws + p.part) : nullptr, p.Kp, p.Gp, p.ksplit, p.tn, p.tm};
     const dim3 grid((unsigned)((int64_t)p.tn * p.tm), (unsigned)p.S);
-    if constexpr (PL == 3) hipLaunchKernelGGL((k_q4_wide<PL, SF32, GROUP, 2, 1, 1, 4, 2, 2>), grid, dim3(256), 0, st, c);
-    else if (p.two) hipLaunchKernelGGL((k_q4_wide<PL, SF32, GROUP, 2, 1, 1, 4, 4, 2>), grid, dim3(256), 0, st, c);
-    else hipLaunchKernelGGL((k_q4_wide<PL, SF32, GROUP, 1, 1, 1, 4, 4, 3>), grid, dim3(256), 0, st, c);
+    if constexpr (PL == 3) hipLaunchKernelGGL((k_q4_wide<-1, PL, SF32, GROUP, 2, 1, 1, 4, 2, 2>), grid, dim3(256), 0, st, c);
+    else if (p.two) hipLaunchKernelGGL((k_q4_wide<-1, PL, SF32, GROUP, 2, 1, 1, 4, 4, 2>), grid, dim3(256), 0, st, c);
+    else if (p.laid) hipLaunchKernelGGL((k_q4_wide<-1, PL, SF32, GROUP, 1, 1, 1, 4, 4, 3>), grid, dim3(256), 0, st, c);
+    else hipLaunchKernelGGL((k_q4_wide<XT, PL, SF32, GROUP, 1, 1, 1, 4, 4, GROUP == 32 ? 2 : 3>), grid, dim3(256), 0, st, c);
     if (p.S > 1) {
         const int64_t n = (int64_t)a.N * a.M, jb = (n + 255) / 256;
         hipLaunchKernelGGL(k_q4_join, dim3((unsigned)(jb < 65536 ? jb : 65536)), dim3(256), 0, st, a,
@@ -1372,8 +1448,8 @@ int seedmm_q4_gemv(const uint32_t* weight, const void* scales, const void* biase
     const int per16 = x_dtype == SEEDMM_F32 ? 4 : x_dtype == SEEDMM_BF16 ? 8 : 16;
     if (N > 1 && ldx % per16 != 0) return SEEDMM_EALIGN;
     const Q4Plan p = q4_plan(x_dtype, group, M, K, N);
-    if (p.wide && (!workspace || workspace_bytes < p.total)) return SEEDMM_EWORKSPACE;
-    if (p.wide && !aligned16(workspace)) return SEEDMM_EALIGN;
+    if (p.total && (!workspace || workspace_bytes < p.total)) return SEEDMM_EWORKSPACE;
+    if (p.total && !aligned16(workspace)) return SEEDMM_EALIGN;
     // one grid's workgroups are counted in 31 bits
     if (p.wide && (int64_t)p.tn * p.tm > 0x7FFFFFFF) return SEEDMM_EINVAL;
     Q4Args a = {weight, scales, biases, x, x_scale, y, M, K, N, ldx, ldy, y_dtype == SEEDMM_BF16};

@@ -19,20 +19,21 @@ int main() {
     void* F = (void*)(uintptr_t)0x100000;   // aligned, never dereferenced (validation fails first)
     const uint32_t* W = (const uint32_t*)F;
     float* X = (float*)F;
-    // sizes: a workspace holds the laid-out rows at least, and none for few rows
+    // sizes: none for few rows; fp32 and many rows are laid out
     for (int i = 0; i < 200000; ++i) {
         const int group = 32 << next32() % 3, dt = next32() % 3;
         const int K = group * (int)(next32() % 600), M = (int)(next32() % 200000), N = (int)(next32() % 5000);
         const size_t n = seedmm_q4_workspace_bytes(dt, group, M, K, N);
         const int pl = dt == SEEDMM_F32 ? 3 : 1;
         if (N * pl <= 16 || M == 0 || K == 0) CHECK(n == 0);
-        else CHECK(n >= (size_t)pl * N * K * 2 && n % 256 == 0);
+        else CHECK(n % 256 == 0);
+        if (N * pl > 16 && M && K && (pl == 3 || (N >= 4096 && M >= 1024))) CHECK(n >= (size_t)pl * N * K * 2);
     }
     CHECK(seedmm_q4_workspace_bytes(SEEDMM_BF16, 64, 1 << 30, 1 << 30, 0x7FFFFFFF) > ((size_t)1 << 40));
     CHECK(seedmm_q4_workspace_bytes(SEEDMM_BF16, 48, 64, 96, 64) == 0);
     // argument errors: each returns before any HIP call
     CHECK(seedmm_q4_gemv(W, F, F, SEEDMM_BF16, 64, F, SEEDMM_BF16, 64, nullptr, F, SEEDMM_F32, 16, 16, 96, 1, nullptr, 0, nullptr) == SEEDMM_EINVAL);
-    CHECK(seedmm_q4_gemv(W, F, F, SEEDMM_BF16, 64, F, SEEDMM_BF16, 64, nullptr, F, SEEDMM_F32, 16, 16, 64, 99, nullptr, 0, nullptr) == SEEDMM_EWORKSPACE);
+    CHECK(seedmm_q4_gemv(W, F, F, SEEDMM_BF16, 64, F, SEEDMM_BF16, 2048, nullptr, F, SEEDMM_F32, 16, 16, 2048, 99, nullptr, 0, nullptr) == SEEDMM_EWORKSPACE);
     CHECK(seedmm_q4_gemv(W, F, F, SEEDMM_BF16, 64, (char*)F + 8, SEEDMM_BF16, 64, nullptr, F, SEEDMM_F32, 16, 16, 64, 1, nullptr, 0, nullptr) == SEEDMM_EALIGN);
     // more than 2^31 tiles
     CHECK(seedmm_q4_gemv(W, F, F, SEEDMM_BF16, 64, F, SEEDMM_BF16, 64, nullptr, F, SEEDMM_F32, 1 << 30, 1 << 30, 64, 0x7FFFFFFF, F, (size_t)-1, nullptr) == SEEDMM_EINVAL);

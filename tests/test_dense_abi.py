@@ -31,8 +31,9 @@ def q4(sm, w=F, s=F, b=F, sd=BF16, group=64, x=F, xd=BF16, ldx=128, xs=None, y=F
     (dict(w=F + 8), -2), (dict(x=F + 8), -2), (dict(s=F + 1), -2), (dict(b=F + 2, sd=F32), -2),
     (dict(y=F + 2), -2), (dict(y=F + 1, yd=BF16), -2), (dict(xd=I8, xs=F + 2), -2),
     (dict(N=2, ldx=132), -2), (dict(N=2, xd=F32, ldx=130), -2), (dict(N=2, xd=I8, xs=F, ldx=136), -2),
-    (dict(N=17, ws=None), -3), (dict(N=17, wsb=100), -3), (dict(N=6, xd=F32, ws=None), -3),
-    (dict(N=17, xd=I8, xs=F, ws=None, wsb=0), -3), (dict(N=17, ws=F + 8), -2),
+    (dict(N=17, K=2048, ldx=2048, ws=None), -3), (dict(N=17, K=2048, ldx=2048, wsb=100), -3),
+    (dict(N=6, xd=F32, ws=None), -3), (dict(N=17, K=2048, ldx=2048, xd=I8, xs=F, ws=None, wsb=0), -3),
+    (dict(N=17, K=2048, ldx=2048, ws=F + 8), -2),
     (dict(M=0, ldy=0, w=None, y=None), 0), (dict(N=0, x=None, y=None), 0),
 ])
 def test_q4_gemv_refusals(sm, kw, expect):
@@ -43,7 +44,10 @@ def test_q4_workspace_sizes(sm):
     f = sm.lib().seedmm_q4_workspace_bytes
     assert [f(BF16, 64, 100, 2048, n) for n in (0, 1, 16)] == [0, 0, 0]
     assert f(F32, 64, 100, 2048, 5) == 0 and f(F32, 64, 100, 2048, 6) >= 3 * 6 * 2048 * 2
-    assert f(BF16, 64, 100, 2048, 17) >= 17 * 2048 * 2 and f(I8, 64, 100, 2048, 17) >= 17 * 2048 * 2
+    # partial sums of at least two splits; laid-out rows of a prompt
+    assert f(BF16, 64, 100, 2048, 17) >= 2 * 17 * 100 * 4 and f(I8, 64, 100, 2048, 17) >= 2 * 17 * 100 * 4
+    assert f(BF16, 64, 100, 64, 17) == 0
+    assert f(BF16, 64, 8192, 2048, 4096) >= 4096 * 2048 * 2
     assert f(BF16, 48, 100, 2048, 17) == 0 and f(BF16, 64, -1, 2048, 17) == 0
     assert f(BF16, 64, 100, 2049, 17) == 0 and f(BF16, 64, 0, 2048, 17) == 0
     assert f(BF16, 64, 1 << 20, 1 << 20, 1 << 20) >= 2 ** 41    # no 32-bit size

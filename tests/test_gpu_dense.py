@@ -515,7 +515,7 @@ def test_binding_refusals_on_gpu_tensors(sm):
     with pytest.raises(ValueError, match="workspace"):
         sm.q4_gemv(mat, x, 16, 64, workspace=torch.zeros(64))
     with pytest.raises(sm.SeedmmError) as e:
-        sm.q4_gemv(mat, x.repeat(20, 1), 16, 64, workspace=torch.zeros(64, device="cuda"))
+        sm.q4_gemv(mat, x.repeat(20, 1).float(), 16, 64, workspace=torch.zeros(64, device="cuda"))
     assert e.value.status == sm.EWORKSPACE
     with pytest.raises(ValueError, match="T..E"):
         sm.route(torch.zeros(8, device="cuda"), 2)
