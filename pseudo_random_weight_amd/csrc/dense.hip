@@ -272,15 +272,16 @@ __global__ __launch_bounds__(kQ4Waves * 64) void k_q4(const Q4Args a, int slab) 
         if (kw * SC < kn) load(kw * SC);
         if (k0) __syncthreads();
         const int per_row = slab / 8, units = a.N * per_row;
-        for (int u0 = tid; u0 < units; u0 += WAVES * 64 * 4) {   // whole waves: units % 64 == 0 or one batch
-            Raw8<XT> raw[4];
+        constexpr int UB = 4;      // pieces in flight a thread
+        for (int u0 = tid; u0 < units; u0 += WAVES * 64 * UB) {
+            Raw8<XT> raw[UB];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < UB; ++i) {
                 const int u = u0 + i * WAVES * 64, t = u / per_row, kk = (u - t * per_row) * 8;
                 raw[i] = load8<XT>(a.x, (int64_t)t * a.ldx + k0 + kk, u < units && kk < kn);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < UB; ++i) {
                 const int u = u0 + i * WAVES * 64, t = u / per_row, kk = (u - t * per_row) * 8;
                 if (u < units) {
                     float sum = place8<XT>(raw[i], xs + t * PL * rowb + kk * EB, rowb);
@@ -1425,7 +1426,8 @@ int seedmm_q4_gemv(const uint32_t* weight, const void* scales, const void* biase
                    int y_dtype, int ldy, int M, int K, int N, void* workspace,
                    size_t workspace_bytes, void* hip_stream) {
     if (group != 32 && group != 64 && group != 128) return SEEDMM_EINVAL;
-    if (M < 0 || K < 0 || N < 0 || M > kMaxDim || K > kMaxDim || K % group != 0 || ldx < K || ldy < M) return SEEDMM_EINVAL;
+    if (M < 0 || K < 0 || N < 0 || M > kMaxDim || K > kMaxDim || N > kMaxDim || K % group != 0 || ldx < K || ldy < M)
+        return SEEDMM_EINVAL;
     if (!float_type(s_dtype) || !float_type(y_dtype)) return SEEDMM_EINVAL;
     if (!float_type(x_dtype) && x_dtype != SEEDMM_I8) return SEEDMM_EINVAL;
     if (M == 0 || N == 0) return SEEDMM_OK;
@@ -1462,7 +1464,7 @@ int seedmm_q4_gemv(const uint32_t* weight, const void* scales, const void* biase
 
 size_t seedmm_q4_workspace_bytes(int x_dtype, int group, int M, int K, int N) {
     if (group != 32 && group != 64 && group != 128) return 0;
-    if (M < 0 || K < 0 || N < 0 || M > kMaxDim || K > kMaxDim || K % group != 0) return 0;
+    if (M < 0 || K < 0 || N < 0 || M > kMaxDim || K > kMaxDim || N > kMaxDim || K % group != 0) return 0;
     return q4_plan(x_dtype, group, M, K, N).total;
 }
 

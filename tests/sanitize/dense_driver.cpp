@@ -29,14 +29,15 @@ int main() {
         else CHECK(n % 256 == 0);
         if (N * pl > 16 && M && K && (pl == 3 || (N >= 4096 && M >= 1024))) CHECK(n >= (size_t)pl * N * K * 2);
     }
-    CHECK(seedmm_q4_workspace_bytes(SEEDMM_BF16, 64, 1 << 30, 1 << 30, 0x7FFFFFFF) > ((size_t)1 << 40));
+    CHECK(seedmm_q4_workspace_bytes(SEEDMM_BF16, 64, 1 << 30, 1 << 30, 1 << 30) > ((size_t)1 << 40));
     CHECK(seedmm_q4_workspace_bytes(SEEDMM_BF16, 48, 64, 96, 64) == 0);
     // argument errors: each returns before any HIP call
     CHECK(seedmm_q4_gemv(W, F, F, SEEDMM_BF16, 64, F, SEEDMM_BF16, 64, nullptr, F, SEEDMM_F32, 16, 16, 96, 1, nullptr, 0, nullptr) == SEEDMM_EINVAL);
     CHECK(seedmm_q4_gemv(W, F, F, SEEDMM_BF16, 64, F, SEEDMM_BF16, 2048, nullptr, F, SEEDMM_F32, 16, 16, 2048, 99, nullptr, 0, nullptr) == SEEDMM_EWORKSPACE);
     CHECK(seedmm_q4_gemv(W, F, F, SEEDMM_BF16, 64, (char*)F + 8, SEEDMM_BF16, 64, nullptr, F, SEEDMM_F32, 16, 16, 64, 1, nullptr, 0, nullptr) == SEEDMM_EALIGN);
     // more than 2^31 tiles
-    CHECK(seedmm_q4_gemv(W, F, F, SEEDMM_BF16, 64, F, SEEDMM_BF16, 64, nullptr, F, SEEDMM_F32, 1 << 30, 1 << 30, 64, 0x7FFFFFFF, F, (size_t)-1, nullptr) == SEEDMM_EINVAL);
+    CHECK(seedmm_q4_gemv(W, F, F, SEEDMM_BF16, 64, F, SEEDMM_BF16, 64, nullptr, F, SEEDMM_F32, 1 << 30, 1 << 30, 64, 1 << 30, F, (size_t)-1, nullptr) == SEEDMM_EINVAL);
+    CHECK(seedmm_q4_workspace_bytes(SEEDMM_BF16, 64, 64, 64, 0x7FFFFFFF) == 0);
     CHECK(seedmm_add_norm(F, SEEDMM_F32, 8, nullptr, 0, 0, nullptr, 0, NAN, nullptr, 0, F, SEEDMM_F32, 8, nullptr, 1, 8, nullptr) == SEEDMM_EINVAL);
     CHECK(seedmm_add_norm(F, SEEDMM_F32, 8, nullptr, 0, 0, nullptr, 0, 1e-6f, nullptr, 0, F, SEEDMM_I8, 8, nullptr, 1, 8, nullptr) == SEEDMM_EINVAL);
     CHECK(seedmm_add_norm(F, SEEDMM_BF16, 8, (char*)F + 1, SEEDMM_BF16, 8, nullptr, 0, 1e-6f, nullptr, 0, F, SEEDMM_F32, 8, nullptr, 1, 8, nullptr) == SEEDMM_EALIGN);

@@ -24,6 +24,7 @@ def q4(sm, w=F, s=F, b=F, sd=BF16, group=64, x=F, xd=BF16, ldx=128, xs=None, y=F
     (dict(K=96), -1), (dict(K=96, group=128), -1),
     (dict(M=-1), -1), (dict(K=-64), -1), (dict(N=-1), -1),
     (dict(M=(1 << 30) + 1, ldy=(1 << 30) + 1), -1), (dict(K=(1 << 30) + 64, ldx=(1 << 30) + 64), -1),
+    (dict(N=(1 << 30) + 1), -1),
     (dict(ldx=127), -1), (dict(ldy=15), -1),
     (dict(sd=I8), -1), (dict(yd=I8), -1), (dict(xd=3), -1), (dict(sd=-1), -1),
     (dict(w=None), -1), (dict(s=None), -1), (dict(b=None), -1), (dict(x=None), -1), (dict(y=None), -1),
