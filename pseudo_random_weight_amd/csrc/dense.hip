@@ -388,7 +388,7 @@ __global__ __launch_bounds__(kQ4Waves * 64) void k_q4(const Q4Args a, int slab) 
 // the accumulators with matrix instructions (3 for 16 groups; 6 with fp32 biases, which
 // are split as well), so the vector units only add s D, one fma an element a 64 columns.
 //
-// A wave holds MT tiles of 32 weight rows by TT tiles of 32 tokens.  Lane r + 32 h loads the
+// A workgroup takes 128 weight rows by 32 TT tokens, a wave 32 of the rows.  Lane r + 32 h loads the
 // 16 bytes of row r that hold columns 32 h .. 32 h + 31 of a 64-column step: word j is its
 // operand of instruction j with no exchange (groups of 32: after one swap of the halves).
 constexpr int kQ4Band = 512;
@@ -449,9 +449,9 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // RAW: the type of activation rows taken as they are (-1: laid out by k_q4_rows).  They are
 // put in the operands' order on their way to LDS, where the groups' sums go as well; the
 // bias term is then one more fma an element and group.
-template <int RAW, int PL, bool SF32, int GROUP, int TT, int MT, int WN, int WM, int SP, int OCC>
-__global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OCC))) void k_q4_wide(const Q4Wide c) {
-    constexpr int BT = 32 * TT * WN, BM = 32 * MT * WM, NTH = 64 * WN * WM;
+template <int RAW, int PL, bool SF32, int GROUP, int TT, int SP, int OCC>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(OCC))) void k_q4_wide(const Q4Wide c) {
+    constexpr int BT = 32 * TT, BM = 128, NTH = 256;
     constexpr int NST = PL * BT * 8 / NTH;      // 16-byte pieces of a step a thread stages
     constexpr int CW = 2 * SP;                  // 16-byte pieces of a weight row in a slab
     constexpr int NWT = BM * CW / NTH;
@@ -459,14 +459,13 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OC
     __shared__ u32x4 xs[SP][PL * BT * 8];
     __shared__ u32x4 ws[BM * CW];
     constexpr bool LAID = RAW < 0;
-    static_assert(LAID || (PL == 1 && TT * MT == 1 && WN == 1), "raw rows: one tile a wave");
+    static_assert(LAID || (PL == 1 && TT == 1), "raw rows: one tile a wave");
     constexpr int XB = RAW == SEEDMM_I8 ? 1 : 2;          // bytes of a staged element
     constexpr int NGB = 64 * SP / GROUP;                  // groups a slab
     __shared__ __align__(16) float gx[LAID ? 1 : NGB][LAID ? 4 : BT];
     const Q4Args& a = c.a;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wn = wave / WM, wm = wave % WM;
     const int r = lane & 31, h = lane >> 5;
     // workgroups of one XCD (every eighth) take neighbouring tiles: columns of kQ4Band tokens
     // by all weight rows, so that its L2 holds the activations of a column
@@ -477,7 +476,7 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OC
     const int col = id / (GT * c.tm), in = id - col * GT * c.tm;
     const int width = min(GT, c.tn - col * GT);
     const int n0 = (col * GT + in % width) * BT;
-    const int64_t mb = (int64_t)(in / width) * BM, m0 = mb + 32 * MT * wm;
+    const int64_t mb = (int64_t)(in / width) * BM, m0 = mb + 32 * wave;
     const int kb = blockIdx.y * c.ksplit, ke = min(a.K, kb + c.ksplit);
     const int G = a.K / GROUP;
 
@@ -498,13 +497,11 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OC
         wsrc[i] = (mb + row < a.M ? mb + row : a.M - 1) * (a.K / 8);
         wdst[i] = piece<CW>(row, u % CW);
     }
-    int64_t row[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) row[mt] = m0 + 32 * mt + r < a.M ? m0 + 32 * mt + r : a.M - 1;
+    const int64_t row = m0 + r < a.M ? m0 + r : a.M - 1;
     constexpr int NG = GROUP == 32 ? 2 : 1;               // groups a step
     constexpr int NGS = 64 * SP >= GROUP ? 64 * SP / GROUP : 1;
     u32x4 stage[SP][NST], wstage[NWT];
-    Scales<SF32, NGS> snext[MT], bnext[LAID ? 1 : MT];
+    Scales<SF32, NGS> snext, bnext;      // (biases with raw rows only)
     // Activations are zero past K.  There the codes of the row's last columns are loaded
     // again, and scales are 0.
     auto fetch = [&](int k) {
@@ -525,11 +522,8 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OC
             const int kw = k + 32 * ((i * NTH + tid) % CW);
             wstage[i] = *(const u32x4*)(a.w + wsrc[i] + (kw < a.K ? kw : a.K - 32) / 8);
         }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            snext[mt].load(a.s, row[mt] * G + k / GROUP, G - k / GROUP);
-            if constexpr (!LAID) bnext[mt].load(a.b, row[mt] * G + k / GROUP, G - k / GROUP);
-        }
+        snext.load(a.s, row * G + k / GROUP, G - k / GROUP);
+        if constexpr (!LAID) bnext.load(a.b, row * G + k / GROUP, G - k / GROUP);
     };
     auto put = [&]() {
 #pragma unroll
@@ -565,51 +559,44 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OC
         for (int i = 0; i < NWT; ++i) ws[wdst[i]] = wstage[i];
     };
 
-    f32x16 acc[TT][MT];
+    f32x16 acc[TT];
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[tt][mt][i] = 0.f;
+        for (int i = 0; i < 16; ++i) acc[tt][i] = 0.f;
     fetch(kb);
     if constexpr (LAID) {   // bias term: the splits take 16 groups in turn
         for (int g0 = 16 * blockIdx.y; g0 < G; g0 += 16 * gridDim.y) {
             const int gl = g0 + 8 * h;
-            bf16x8 bb[MT][SF32 ? 3 : 1];
+            bf16x8 bb[SF32 ? 3 : 1];
+            Scales<SF32, 8> b;
+            b.load(a.b, row * G + min(gl, G), G - min(gl, G));
+            if constexpr (SF32) {
+                uint32_t p[8][3];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                Scales<SF32, 8> b;
-                b.load(a.b, row[mt] * G + min(gl, G), G - min(gl, G));
-                if constexpr (SF32) {
-                    uint32_t p[8][3];
+                for (int i = 0; i < 8; ++i) split3(b.get(i), p[i]);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) split3(b.get(i), p[i]);
+                for (int q = 0; q < 3; ++q) {
+                    u32x4 o;
 #pragma unroll
-                    for (int q = 0; q < 3; ++q) {
-                        u32x4 o;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[i] = (p[2 * i][q] >> 16) | p[2 * i + 1][q];
-                        bb[mt][q] = __builtin_bit_cast(bf16x8, o);
-                    }
-                } else {
-                    bb[mt][0] = __builtin_bit_cast(bf16x8, u32x4{b.u[0], b.u[1], b.u[2], b.u[3]});
+                    for (int i = 0; i < 4; ++i) o[i] = (p[2 * i][q] >> 16) | p[2 * i + 1][q];
+                    bb[q] = __builtin_bit_cast(bf16x8, o);
                 }
+            } else {
+                bb[0] = __builtin_bit_cast(bf16x8, u32x4{b.u[0], b.u[1], b.u[2], b.u[3]});
             }
 #pragma unroll
             for (int tt = 0; tt < TT; ++tt) {
-                const int n = min(n0 + 32 * (TT * wn + tt) + r, a.N - 1);
+                const int n = min(n0 + 32 * tt + r, a.N - 1);
                 bf16x8 xa[3];
 #pragma unroll
                 for (int p = 0; p < 3; ++p)
                     xa[p] = *(const bf16x8*)(c.xg + ((int64_t)p * a.N + n) * c.Gp + gl);
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int q = 0; q < (SF32 ? 3 : 1); ++q)
 #pragma unroll
-                    for (int q = 0; q < (SF32 ? 3 : 1); ++q)
-#pragma unroll
-                        for (int p = 0; p + q < 3; ++p)
-                            acc[tt][mt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[p], bb[mt][q], acc[tt][mt], 0, 0, 0);
+                    for (int p = 0; p + q < 3; ++p)
+                        acc[tt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[p], bb[q], acc[tt], 0, 0, 0);
             }
         }
     }
@@ -618,56 +605,46 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OC
 
     // Tile i's chain of instructions runs while the vector units add tile i - 1 (the last
     // tile's addition is carried into the next step) and unpack the next codes.
-    constexpr int NT = TT * MT, JC = 4 / NG;   // tiles; instructions a group
-    static_assert(NT == 1 || NT % 2 == 0, "the carried tile's sums are not the first's");
+    constexpr int JC = 4 / NG, LAST = TT == 1 ? 1 : (TT - 1) & 1;   // instructions a group; the carried d
+    static_assert(TT == 1 || TT % 2 == 0, "the carried tile's sums are not the first's");
     f32x16 d[2][NG];
     float sp[NG];                              // the carried tile's scales
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         sp[g] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) d[NT == 1 ? 1 : (NT - 1) & 1][g][i] = 0.f;
+        for (int i = 0; i < 16; ++i) d[LAST][g][i] = 0.f;
     }
     // A slab's activations, codes and scales are loaded while the one before is multiplied
     // and take its place in LDS after it.
-    Scales<SF32, NGS> sc[MT], bc[LAID ? 1 : MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) sc[mt] = snext[mt];
-    if constexpr (!LAID) bc[0] = bnext[0];
+    Scales<SF32, NGS> sc = snext, bc;
+    if constexpr (!LAID) bc = bnext;
     auto step = [&](int b) {
-        uint32_t w[MT][4];
-        float s[MT][NG];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const int wr = 32 * (MT * wm + mt) + r;
-            const u32x4 wv = ws[piece<CW>(wr, 2 * b + h)];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[mt][j] = wv[j];
-#pragma unroll
-            for (int g = 0; g < NG; ++g) s[mt][g] = sc[mt].get(64 * b / GROUP + g);
+        const int wr = 32 * wave + r;
+        const u32x4 wv = ws[piece<CW>(wr, 2 * b + h)];
+        uint32_t w[4] = {wv[0], wv[1], wv[2], wv[3]};
+        if constexpr (GROUP == 32) {
+            auto x = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+            auto y = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+            w[0] = x[0]; w[2] = x[1]; w[1] = y[0]; w[3] = y[1];
         }
-        bf16x8 bq[MT][4], xa[PL][4];
+        float s[NG];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const int tt = i / MT, mt = i % MT;
-            if (mt == 0) {
-                const int t = 32 * (TT * wn + tt) + r;
+        for (int g = 0; g < NG; ++g) s[g] = sc.get(64 * b / GROUP + g);
+        bf16x8 bq[4], xa[PL][4];
 #pragma unroll
-                for (int p = 0; p < PL; ++p)
+        for (int tt = 0; tt < TT; ++tt) {
+            const int t = 32 * tt + r;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int ch = GROUP == 32 ? 4 * (j >> 1) + 2 * h + (j & 1) : 4 * h + j;
-                        xa[p][j] = __builtin_bit_cast(bf16x8, xs[b][piece<8>(p * BT + t, ch)]);
-                    }
-            }
-            if (tt == 0) {
-                if constexpr (GROUP == 32) {
-                    auto x = __builtin_amdgcn_permlane32_swap(w[mt][0], w[mt][2], false, false);
-                    auto y = __builtin_amdgcn_permlane32_swap(w[mt][1], w[mt][3], false, false);
-                    w[mt][0] = x[0]; w[mt][2] = x[1]; w[mt][1] = y[0]; w[mt][3] = y[1];
+            for (int p = 0; p < PL; ++p)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int ch = GROUP == 32 ? 4 * (j >> 1) + 2 * h + (j & 1) : 4 * h + j;
+                    xa[p][j] = __builtin_bit_cast(bf16x8, xs[b][piece<8>(p * BT + t, ch)]);
                 }
+            if (tt == 0) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) bq[mt][j] = codes_bf16(w[mt][j]);
+                for (int j = 0; j < 4; ++j) bq[j] = codes_bf16(w[j]);
             }
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
@@ -676,18 +653,18 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OC
                 for (int p = 0; p < PL; ++p)
 #pragma unroll
                     for (int j = g * JC; j < (g + 1) * JC; ++j)
-                        e = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[p][j], bq[mt][j], e, 0, 0, 0);
-                d[i & 1][g] = e;
+                        e = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[p][j], bq[j], e, 0, 0, 0);
+                d[tt & 1][g] = e;
             }
-            const int q = (i + NT - 1) % NT, qt = q / MT, qm = q % MT;   // the tile before
+            const int q = (tt + TT - 1) % TT;      // the tile before
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                const float sq = i == 0 ? sp[g] : s[qm][g];
+                const float sq = tt == 0 ? sp[g] : s[g];
 #pragma unroll
                 for (int v = 0; v < 16; ++v)
-                    acc[qt][qm][v] = __builtin_fmaf(sq, d[NT == 1 ? 1 : q & 1][g][v], acc[qt][qm][v]);
+                    acc[q][v] = __builtin_fmaf(sq, d[tt == 0 ? LAST : q & 1][g][v], acc[q][v]);
             }
-            if constexpr (NT == 1) {
+            if constexpr (TT == 1) {
 #pragma unroll
                 for (int g = 0; g < NG; ++g) d[1][g] = d[0][g];
             }
@@ -696,24 +673,24 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OC
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 if (GROUP == 128 && (b & 1)) continue;
-                const float bv = bc[0].get(64 * b / GROUP + g);
+                const float bv = bc.get(64 * b / GROUP + g);
                 const float* const x = gx[64 * b / GROUP + g];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const f32x4 X = *(const f32x4*)(x + 8 * q + 4 * h);
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
-                        acc[0][0][4 * q + v] = __builtin_fmaf(bv, X[v], acc[0][0][4 * q + v]);
+                        acc[0][4 * q + v] = __builtin_fmaf(bv, X[v], acc[0][4 * q + v]);
                 }
             }
         }
 #pragma unroll
-        for (int g = 0; g < NG; ++g) sp[g] = s[MT - 1][g];
+        for (int g = 0; g < NG; ++g) sp[g] = s[g];
         // spread the vector work between the instructions of a step (4096 x 8192 x 2048:
         // 200 -> 185 us; one tile a wave gains nothing by it)
         if constexpr (TT == 2 && PL == 1) {
 #pragma unroll
-            for (int i = 0; i < 4 * NT; ++i) {
+            for (int i = 0; i < 4 * TT; ++i) {
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
                 __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
             }
@@ -728,9 +705,8 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OC
         if (more) {
             __syncthreads();
             put();
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) sc[mt] = snext[mt];
-            if constexpr (!LAID) bc[0] = bnext[0];
+            sc = snext;
+            if constexpr (!LAID) bc = bnext;
             __syncthreads();
         }
     }
@@ -738,28 +714,22 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(OC
     for (int g = 0; g < NG; ++g)
 #pragma unroll
         for (int v = 0; v < 16; ++v)
-            acc[TT - 1][MT - 1][v] =
-                __builtin_fmaf(sp[g], d[NT == 1 ? 1 : (NT - 1) & 1][g][v], acc[TT - 1][MT - 1][v]);
+            acc[TT - 1][v] = __builtin_fmaf(sp[g], d[LAST][g][v], acc[TT - 1][v]);
 
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const int n = n0 + 32 * (TT * wn + tt) + 8 * (i >> 2) + 4 * h + (i & 3);
-            if (n >= a.N) continue;
-            const float xsc = a.xs && !c.part ? a.xs[n] : 1.0f;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                const int64_t m = m0 + 32 * mt + r;
-                if (m >= a.M) continue;
-                const float v = acc[tt][mt][i] * xsc;
-                if (c.part) {
-                    c.part[((int64_t)blockIdx.y * a.N + n) * a.M + m] = v;
-                } else {
-                    const int64_t o = (int64_t)n * a.ldy + m;
-                    if (a.y_bf16) ((uint16_t*)a.y)[o] = f32_to_bf16(v);
-                    else ((float*)a.y)[o] = v;
-                }
+            const int n = n0 + 32 * tt + 8 * (i >> 2) + 4 * h + (i & 3);
+            const int64_t m = m0 + r;
+            if (n >= a.N || m >= a.M) continue;
+            if (c.part) {
+                c.part[((int64_t)blockIdx.y * a.N + n) * a.M + m] = acc[tt][i];
+            } else {
+                const float v = a.xs ? acc[tt][i] * a.xs[n] : acc[tt][i];
+                const int64_t o = (int64_t)n * a.ldy + m;
+                if (a.y_bf16) ((uint16_t*)a.y)[o] = f32_to_bf16(v);
+                else ((float*)a.y)[o] = v;
             }
         }
 }
@@ -1367,10 +1337,10 @@ void launch_q4_group(const Q4Args& a, const Q4Plan& p, void* ws, hipStream_t st)
     }
     Q4Wide c = {a, xp, xg, p.S > 1 ? (float*)((char*)ws + p.part) : nullptr, p.Kp, p.Gp, p.ksplit, p.tn, p.tm};
     const dim3 grid((unsigned)((int64_t)p.tn * p.tm), (unsigned)p.S);
-    if constexpr (PL == 3) hipLaunchKernelGGL((k_q4_wide<-1, PL, SF32, GROUP, 2, 1, 1, 4, 2, 2>), grid, dim3(256), 0, st, c);
-    else if (p.two) hipLaunchKernelGGL((k_q4_wide<-1, PL, SF32, GROUP, 2, 1, 1, 4, 4, 2>), grid, dim3(256), 0, st, c);
-    else if (p.laid) hipLaunchKernelGGL((k_q4_wide<-1, PL, SF32, GROUP, 1, 1, 1, 4, 4, 3>), grid, dim3(256), 0, st, c);
-    else hipLaunchKernelGGL((k_q4_wide<XT, PL, SF32, GROUP, 1, 1, 1, 4, 4, GROUP == 32 ? 2 : 3>), grid, dim3(256), 0, st, c);
+    if constexpr (PL == 3) hipLaunchKernelGGL((k_q4_wide<-1, PL, SF32, GROUP, 2, 2, 2>), grid, dim3(256), 0, st, c);
+    else if (p.two) hipLaunchKernelGGL((k_q4_wide<-1, PL, SF32, GROUP, 2, 4, 2>), grid, dim3(256), 0, st, c);
+    else if (p.laid) hipLaunchKernelGGL((k_q4_wide<-1, PL, SF32, GROUP, 1, 4, 3>), grid, dim3(256), 0, st, c);
+    else hipLaunchKernelGGL((k_q4_wide<XT, PL, SF32, GROUP, 1, 4, GROUP == 32 ? 2 : 3>), grid, dim3(256), 0, st, c);
     if (p.S > 1) {
         const int64_t n = (int64_t)a.N * a.M, jb = (n + 255) / 256;
         hipLaunchKernelGGL(k_q4_join, dim3((unsigned)(jb < 65536 ? jb : 65536)), dim3(256), 0, st, a,
