@@ -217,7 +217,7 @@ __device__ __forceinline__ float place8_as_bf16(const Raw8<SEEDMM_I8>& x, char* 
 // cache lines, and the wave's own piece of LDS hands them to the lanes that multiply them
 // (each lane loading its own 16 bytes, 64 bytes a row, took 54 us for 131072 x 2048 at one
 // token against 30 us: the texture path passes one line at a time).  That size streams
-// its 152 MB at 5.0 TB/s, what a large copy reaches; small matrices are bound by the
+// its 152 MB at 5.2 TB/s with 3 sets of inputs in turn, 4.3 with 8; small matrices are bound by the
 // latency of one launch and two dependent loads (100 x 2048: 3.4 us, 2048 x 2048: 3.5 us).
 // The D tile of 16x16x32 instructions has a row a token: up to 4 activation rows sit in D
 // rows 0, 4, 8, 12 (JN = 1), so each lane scales one value a group instead of four.
@@ -687,7 +687,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(OCC))) void
 #pragma unroll
         for (int g = 0; g < NG; ++g) sp[g] = s[g];
         // spread the vector work between the instructions of a step (4096 x 8192 x 2048:
-        // 200 -> 185 us; one tile a wave gains nothing by it)
+        // 200 -> 190 us; one tile a wave gains nothing by it)
         if constexpr (TT == 2 && PL == 1) {
 #pragma unroll
             for (int i = 0; i < 4 * TT; ++i) {
@@ -1294,8 +1294,8 @@ Q4Plan q4_plan(int x_dtype, int group, int M, int K, int N) {
     p.Gp = (K / group + 15) / 16 * 16;
     // Tiles of 64 tokens by 128 weight rows where they make 512 workgroups (two a CU);
     // else of 32 by 128 with K split until they do (256 x 8192 x 2048: 26 us against 31;
-    // 61 x 5125 x 4160: one split 73 us, seven 24 us).  fp32 rows are three planes of work:
-    // always 64.
+    // 61 x 5125 x 4160: one split 73 us, seven 24 us; as first built).  fp32 rows are three
+    // planes of work: always 64.
     const int64_t tm = ((int64_t)M + 127) / 128;
     p.two = PL == 3 || (((int64_t)N + 63) / 64) * tm >= 512;
     const int BT = p.two ? 64 : 32, slab = PL == 3 ? 128 : 256;
@@ -1309,8 +1309,8 @@ Q4Plan q4_plan(int x_dtype, int group, int M, int K, int N) {
     p.ksplit = per * slab;
     p.S = (slabs + per - 1) / per;
     // A launch that lays the rows out costs about 3 us; in the product it is done once a row
-    // tile (61 x 5125 x 4160, 10 million elements so: 23.0 us laid out, 20.5 not; 64 x 8192 x
-    // 8192, 34 million: 31.8 and 33.9; 4096 x 100 x 2048, 8 million: 24.0 and 17.4).
+    // tile (61 x 5125 x 4160, 10 million elements so: 20.4 us laid out, 20.0 not; 64 x 8192 x
+    // 8192, 34 million: 31.0 and 33.4; 4096 x 100 x 2048, 8 million: 23.4 and 16.1).
     p.laid = p.two || (int64_t)N * K > (1 << 24) / tm;
     if (p.laid) {
         p.xg = align_up((size_t)PL * (size_t)N * (size_t)p.Kp * 2);
