@@ -989,13 +989,14 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_add_norm(const NormAr
     }
 }
 
-// Rows of any length, read twice.
+// Rows of any length, read twice.  (The step past the end of a row of nearly 2^31 elements
+// needs more than 31 bits.)
 __global__ __launch_bounds__(1024) void k_add_norm_long(const NormArgs a) {
     __shared__ float red[2][16];
     const int64_t n = blockIdx.x;
     float ss = 0.f, top = 0.f;
     bool bad = false;
-    for (int h = threadIdx.x; h < a.H; h += 1024) {
+    for (int64_t h = threadIdx.x; h < a.H; h += 1024) {
         float r = load_el(a.x, a.x_dt, n * a.ldx + h);
         if (a.d) r += load_el(a.d, a.d_dt, n * a.ldd + h);
         const float v = a.w ? r * load_el(a.w, a.w_dt, h) : r;
@@ -1011,7 +1012,7 @@ __global__ __launch_bounds__(1024) void k_add_norm_long(const NormArgs a) {
     for (int i = 1; i < 16; ++i) { ss += red[0][i]; top = fmaxf(top, red[1][i]); }
     const RowFactor o = row_factor(a, ss, top);
     if (a.out_dt == SEEDMM_I8 && threadIdx.x == 0) a.scale[n] = o.sc;
-    for (int h = threadIdx.x; h < a.H; h += 1024) {
+    for (int64_t h = threadIdx.x; h < a.H; h += 1024) {
         float r = load_el(a.x, a.x_dt, n * a.ldx + h);
         if (a.d) r += load_el(a.d, a.d_dt, n * a.ldd + h);
         const float v = (a.w ? r * load_el(a.w, a.w_dt, h) : r) * o.f;

@@ -1,0 +1,34 @@
+"""GPU tests of the dense operators at the limits of what their calls accept: the longest
+rows, values at the ends of the types' ranges, and what the Python entries refuse.
+Tolerances are those of test_gpu_dense."""
+import math
+
+import pytest
+
+from test_gpu_dense import norm_tol, say, sm  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def test_norm_of_the_longest_row(sm):
+    """H = 2^31 - 1: a thread's index passes 31 bits in the step that ends its loop."""
+    import torch
+    H = 2 ** 31 - 1
+    say("norm", 1, H)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(61)
+    x = torch.empty(H + 64, dtype=torch.bfloat16, device="cuda")
+    x.normal_(generator=g)
+    out = torch.full((H + 64,), 9.0, dtype=torch.bfloat16, device="cuda")
+    kept = x[H:].clone()
+    sm.add_norm(x[:H], out=out[:H])
+    torch.cuda.synchronize()
+    step = 2 ** 26
+    ss = sum(float((x[i:min(i + step, H)].double() ** 2).sum()) for i in range(0, H, step))
+    f = 1 / math.sqrt(ss / H + 1e-6)
+    tol = norm_tol(H)
+    for i in range(0, H, step):
+        v = x[i:min(i + step, H)].double() * f
+        err = (out[i:min(i + step, H)].double() - v).abs()
+        assert bool((err <= (tol + 2.0 ** -8 * (1 + tol)) * v.abs() + 1e-37).all()), i
+    assert bool((out[H:] == 9).all()) and bool((x[H:] == kept).all())
