@@ -794,8 +794,10 @@ class MoeBlock:
             _flat(ids, _INT32, T * self.top_k, "ids", dev)
         if w is not None:
             _flat(w, _FP32, T * self.top_k, "w", dev)
-        if workspace.get_device() != dev:
-            raise ValueError("the workspace is on another device")
+        if not isinstance(workspace, torch.Tensor):
+            raise TypeError("the workspace must be a tensor")
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("the workspace must be a contiguous tensor on the layer's device")
         sd = None if side is None else ctypes.byref(side.c())
         ptr = lambda t: None if t is None else t.data_ptr()
         handle = _handle(stream, r)

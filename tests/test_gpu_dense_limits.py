@@ -5,7 +5,7 @@ import math
 
 import pytest
 
-from test_gpu_dense import norm_tol, say, sm  # noqa: F401
+from test_gpu_dense import block_case, norm_tol, say, sm  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +32,24 @@ def test_norm_of_the_longest_row(sm):
         err = (out[i:min(i + step, H)].double() - v).abs()
         assert bool((err <= (tol + 2.0 ** -8 * (1 + tol)) * v.abs() + 1e-37).all()), i
     assert bool((out[H:] == 9).all()) and bool((x[H:] == kept).all())
+
+
+def test_block_refuses_a_workspace_that_is_not_its_size(sm):
+    """A workspace whose elements share memory, or lie apart, holds fewer bytes than it has
+    elements: the layer would write past it."""
+    import torch
+    blk = block_case(sm, 8, 128, 64, 4, 2, "softmax", 1)[0]
+    r = torch.zeros(3, 128, device="cuda")
+    n = blk.workspace_bytes(3)
+    one = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    for bad in (one[:1].expand(n), torch.zeros(2 * n, dtype=torch.uint8, device="cuda")[::2],
+                torch.zeros(n, dtype=torch.uint8)):
+        with pytest.raises(ValueError, match="workspace"):
+            blk.moe(r, workspace=bad)
+    with pytest.raises(TypeError, match="workspace"):
+        blk.moe(r, workspace=one.data_ptr())
+    with pytest.raises(sm.SeedmmError) as e:
+        blk.moe(r, workspace=one)
+    assert e.value.status == sm.EWORKSPACE
+    torch.cuda.synchronize()
+    assert bool((one == 0).all()) and bool((r == 0).all())
