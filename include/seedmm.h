@@ -464,7 +464,8 @@ int seedmm_add_norm(const void *x, int x_dtype, int64_t ldx, const void *delta, 
  * chosen logits is this library's reading for the others):
  *   SEEDMM_SOFTMAX: the top_k largest logits of a token; weights = softmax over those.
  *   SEEDMM_SIGMOID: the top_k largest sigmoid(logit) + bias (bias fp32[E] or NULL; compared
- *   in 64 bits); weights = sigmoid(logit) over their sum, without the bias.
+ *   in 64 bits); weights = sigmoid(logit) over their sum, without the bias.  Sigmoids are
+ *   64-bit numbers: where every chosen logit is below -709 they are 0, and so are the weights.
  *   logits: [T][ldl] fp32 or bf16;  ids: int32[T][top_k], w: fp32[T][top_k], in falling
  *   order of score; equal scores go to the lower expert first.
  *   A logit of -inf or NaN (and a bias of -inf or NaN) masks its expert.  Where fewer than

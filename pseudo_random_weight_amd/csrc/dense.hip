@@ -1232,6 +1232,15 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
     float w;
     if constexpr (SIG) {
         w = (float)p;
+        // From logits of -60 up a sigmoid is an ordinary fp32 number (2^-87 at least); far below it
+        // has fewer bits there, then none (e^-104): shares of the largest then, divided in 64 bits.
+        if (__any(weighs && ml < -60.f)) {
+            const uint64_t u = weighs ? (uint64_t)__double_as_longlong(p) : 0;   // p >= 0: in order
+            const uint32_t hi = wave_umax((uint32_t)(u >> 32));
+            const uint32_t lo = wave_umax((uint32_t)(u >> 32) == hi ? (uint32_t)u : 0u);
+            const double most = __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+            w = most > 0.0 ? (float)(p / most) : 0.f;
+        }
     } else {
         const float m = wave_max(weighs ? ml : -INFINITY);
         w = ml == m ? 1.0f : expf(ml - m);

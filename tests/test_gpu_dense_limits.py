@@ -5,7 +5,7 @@ import math
 
 import pytest
 
-from test_gpu_dense import block_case, norm_tol, say, sm  # noqa: F401
+from test_gpu_dense import block_case, check_route, gen, norm_tol, say, sm  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +53,29 @@ def test_block_refuses_a_workspace_that_is_not_its_size(sm):
     assert e.value.status == sm.EWORKSPACE
     torch.cuda.synchronize()
     assert bool((one == 0).all()) and bool((r == 0).all())
+
+
+@pytest.mark.parametrize("E,k", [(3, 3), (40, 8), (100, 8), (512, 10), (512, 64), (4096, 64)])
+def test_route_weights_of_tiny_sigmoids(sm, E, k):
+    """Sigmoids below what fp32 holds: the weights are still their share of the sum, to 16 u
+    (two roundings of the quotients, at most 6 of the sum, one of the division)."""
+    import torch
+    g = gen(62)
+    noise = torch.randn(E, generator=g)
+    rows = [noise - c for c in (60.0, 69.0, 88.0, 95.0, 104.0, 120.0, 400.0, 700.0)]
+    rows += [torch.full((E,), -120.0), torch.linspace(-100, -102, E), torch.linspace(-40, -110, E)]
+    for i in range(3):                 # masked among them, fewer than top_k left, one large
+        r = noise - 130
+        r[i::3 - i] = -math.inf
+        rows.append(r)
+    r = torch.full((E,), -math.inf)
+    r[E - 1], r[E // 2] = -100.0, -101.0
+    rows.append(r)
+    r = noise - 100
+    r[E // 3] = 0.5
+    rows.append(r)
+    lg = torch.stack(rows)
+    bias = 0.1 * torch.randn(E, generator=g)
+    for dt in (torch.float32, torch.bfloat16):
+        check_route(sm, lg.to(dt), k, "sigmoid")
+        check_route(sm, lg.to(dt), k, "sigmoid", bias)
