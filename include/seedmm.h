@@ -445,8 +445,10 @@ size_t seedmm_q4_workspace_bytes(int x_dtype, int group, int M, int K, int N);
  *   SEEDMM_I8: codes round(value / scale[n]) in [-127, 127] with scale[n] = max_h |value| /
  *   127 (at least 2^-126); a row that holds an infinity or NaN gets scale NaN and codes 0.
  *   scale: fp32[N] with SEEDMM_I8, NULL otherwise.
- *   r is not rounded before the norm (only where it is stored as bf16); the sum of squares
- *   is fp32, so a row whose sum of squares passes 3.4e38 has no meaning.  Rows of any ld
+ *   r is an fp32 sum, not rounded further before the norm (only where it is stored as bf16).
+ *   Squares are summed in fp32, of a row taken times a power of two where fp32 does not hold
+ *   them, so finite rows of any size have their norm; r times weight has to be an fp32 number,
+ *   and a row of zeros with eps = 0 has no value (0/0).  Rows of any ld
  *   and alignment are taken; rows that start on 16 bytes are faster.  Elements past H are
  *   left as they were.
  * Errors: SEEDMM_EINVAL (null pointer, N or H < 0, ld < H, bad dtype, eps negative or not

@@ -799,7 +799,9 @@ __device__ __forceinline__ uint32_t wave_umin(uint32_t v) {
 // seedmm_add_norm.  r = x + delta in fp32; out = r rsqrt(mean r^2 + eps) w.  The 8-bit
 // scale is max |r w| times the row's factor over 127: one pass finds both statistics, and
 // a row stays in registers between its load and its store (rows up to 32,768 elements;
-// longer ones are read twice).
+// longer ones are read twice).  A row whose mean square fp32 does not hold is multiplied by
+// a power of two, exactly, and summed again (asking for it costs 0.07 us of 2.6 at one token
+// and nothing that shows at 4096 x 2048).
 // ----------------------------------------------------------------------------------
 struct NormArgs {
     const void* x;
@@ -876,18 +878,24 @@ __device__ __forceinline__ void store8(void* p, int64_t i, int n, const float (&
     }
 }
 
-// The row's factor, and for 8 bits its scale and the scale's reciprocal (0: codes 0).
-struct RowFactor {
-    float f, sc, inv;
+// The mean square plus eps, where fp32 holds it: below 2^-100 the squares' underflow (2^-126 at
+// most a square) could show in it, above the squares overflow.
+__device__ __forceinline__ bool mean_holds(float t) { return t >= 0x1p-100f && t < INFINITY; }
+// The factor of a row outside of that from the sum of its squares, the row taken times 2^up.
+__device__ __forceinline__ float scaled_factor(const NormArgs& a, float ss, int up) {
+    return (float)(1.0 / sqrt((double)ss / (double)a.H + ldexp((double)a.eps, 2 * up)));
+}
+
+// For 8 bits a row's scale and the scale's reciprocal (0: codes 0).
+struct RowScale {
+    float sc, inv;
 };
-__device__ __forceinline__ RowFactor row_factor(const NormArgs& a, float ss, float top) {
-    RowFactor o;
-    o.f = 1.0f / sqrtf(ss / (float)a.H + a.eps);
-    o.sc = o.inv = 0.f;
+__device__ __forceinline__ RowScale row_scale(const NormArgs& a, float f, float top) {
+    RowScale o = {0.f, 0.f};
     if (a.out_dt == SEEDMM_I8) {
-        o.sc = fmaxf(top * o.f / 127.0f, 1.17549435e-38f);
+        o.sc = fmaxf(top * f / 127.0f, 1.17549435e-38f);
         // a row with an infinity or NaN: codes 0 and scale NaN
-        if (!(top * o.f < INFINITY)) o.sc = NAN;
+        if (!(top * f < INFINITY)) o.sc = NAN;
         o.inv = o.sc == o.sc ? 1.0f / o.sc : 0.f;
     }
     return o;
@@ -937,7 +945,6 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_add_norm(const NormAr
         }
     }
     float r[NP][8], ss = 0.f, top = 0.f;
-    bool bad = false;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
 #pragma unroll
@@ -951,24 +958,73 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_add_norm(const NormAr
             ss = __builtin_fmaf(v, v, ss);
         }
         if (a.res && cnt[p] > 0) store8<XT>(a.res, n * a.ldr + (p * TPR + tid) * 8, cnt[p], r[p]);
+    }
+    auto weighted = [&]() {     // max |r w| of this thread; infinite where one is not finite
+        float m = 0.f;
+        bool bad = false;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            r[p][j] *= w[p][j];
-            top = fmaxf(top, fabsf(r[p][j]));
-            bad |= !(fabsf(r[p][j]) < INFINITY);
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float v = fabsf(r[p][j] * w[p][j]);
+                m = fmaxf(m, v);
+                bad |= !(v < INFINITY);
+            }
+        return bad ? INFINITY : m;
+    };
+    auto row_stats = [&]() {    // both statistics over the row's threads
+        ss = wave_sum(ss);
+        if (a.out_dt == SEEDMM_I8) top = wave_max(top);
+        if constexpr (NW > 1) {
+            const int wave = threadIdx.x >> 6;
+            if ((threadIdx.x & 63) == 0) { red[0][wave] = ss; red[1][wave] = top; }
+            __syncthreads();
+            ss = red[0][0]; top = red[1][0];
+#pragma unroll
+            for (int i = 1; i < NW; ++i) { ss += red[0][i]; top = fmaxf(top, red[1][i]); }
+        }
+    };
+    if (a.out_dt == SEEDMM_I8) top = weighted();
+    row_stats();
+    const float t = ss / (float)a.H + a.eps;
+    float f = 1.0f / sqrtf(t);
+    const bool out_of_range = !mean_holds(t) || (a.out_dt == SEEDMM_I8 && !(top < INFINITY));
+    if (__builtin_expect(__builtin_amdgcn_readfirstlane(out_of_range), 0)) {   // (all of the row's threads)
+        float big = 0.f;
+        bool bad = false;
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                big = fmaxf(big, fabsf(r[p][j]));
+                bad |= !(fabsf(r[p][j]) < INFINITY);
+            }
+        big = wave_max(bad ? INFINITY : big);
+        if constexpr (NW > 1) {
+            __syncthreads();    // the statistics have been read
+            if ((threadIdx.x & 63) == 0) red[0][threadIdx.x >> 6] = big;
+            __syncthreads();
+            big = red[0][0];
+#pragma unroll
+            for (int i = 1; i < NW; ++i) big = fmaxf(big, red[0][i]);
+            __syncthreads();
+        }
+        if (big > 0.f && big < INFINITY) {
+            const int up = -ilogbf(big);
+            ss = 0.f;
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    r[p][j] = ldexpf(r[p][j], up);
+                    ss = __builtin_fmaf(r[p][j], r[p][j], ss);
+                }
+            top = a.out_dt == SEEDMM_I8 ? weighted() : 0.f;
+            row_stats();
+            f = scaled_factor(a, ss, up);
         }
     }
-    ss = wave_sum(ss);
-    if (a.out_dt == SEEDMM_I8) top = wave_max(bad ? INFINITY : top);
-    if constexpr (NW > 1) {
-        const int wave = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0) { red[0][wave] = ss; red[1][wave] = top; }
-        __syncthreads();
-        ss = red[0][0]; top = red[1][0];
-#pragma unroll
-        for (int i = 1; i < NW; ++i) { ss += red[0][i]; top = fmaxf(top, red[1][i]); }
-    }
-    const RowFactor o = row_factor(a, ss, top);
+    const RowScale o = row_scale(a, f, top);
     if (a.out_dt == SEEDMM_I8 && tid == 0) a.scale[n] = o.sc;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
@@ -976,7 +1032,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_add_norm(const NormAr
         const int64_t at = n * a.ldo + (p * TPR + tid) * 8;
         float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = r[p][j] * o.f;
+        for (int j = 0; j < 8; ++j) v[j] = r[p][j] * w[p][j] * f;
         if (a.out_dt == SEEDMM_I8) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = code_of(v[j], o.inv);
@@ -989,33 +1045,55 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_add_norm(const NormAr
     }
 }
 
-// Rows of any length, read twice.  (The step past the end of a row of nearly 2^31 elements
+// Rows of any length, read twice (four times outside of fp32's range).  (The step past the end of a row of nearly 2^31 elements
 // needs more than 31 bits.)
 __global__ __launch_bounds__(1024) void k_add_norm_long(const NormArgs a) {
     __shared__ float red[2][16];
     const int64_t n = blockIdx.x;
-    float ss = 0.f, top = 0.f;
-    bool bad = false;
-    for (int64_t h = threadIdx.x; h < a.H; h += 1024) {
-        float r = load_el(a.x, a.x_dt, n * a.ldx + h);
-        if (a.d) r += load_el(a.d, a.d_dt, n * a.ldd + h);
-        const float v = a.w ? r * load_el(a.w, a.w_dt, h) : r;
-        ss = __builtin_fmaf(r, r, ss);
-        top = fmaxf(top, fabsf(v));
-        bad |= !(fabsf(v) < INFINITY);
+    // max |r w| and the sum of squares of the row times 2^up, or max |r| (up: NULL); infinite
+    // where one is not finite
+    float ss, top;
+    auto pass = [&](const int* up) {
+        ss = top = 0.f;
+        bool bad = false;
+        for (int64_t h = threadIdx.x; h < a.H; h += 1024) {
+            float r = load_el(a.x, a.x_dt, n * a.ldx + h);
+            if (a.d) r += load_el(a.d, a.d_dt, n * a.ldd + h);
+            if (up) r = ldexpf(r, *up);
+            const float v = up && a.w ? r * load_el(a.w, a.w_dt, h) : r;
+            ss = __builtin_fmaf(r, r, ss);
+            top = fmaxf(top, fabsf(v));
+            bad |= !(fabsf(v) < INFINITY);
+        }
+        ss = wave_sum(ss);
+        top = wave_max(bad ? INFINITY : top);
+        __syncthreads();    // the pass before has been read
+        if ((threadIdx.x & 63) == 0) { red[0][threadIdx.x >> 6] = ss; red[1][threadIdx.x >> 6] = top; }
+        __syncthreads();
+        ss = red[0][0]; top = red[1][0];
+        for (int i = 1; i < 16; ++i) { ss += red[0][i]; top = fmaxf(top, red[1][i]); }
+    };
+    int up = 0;
+    pass(&up);
+    const float t = ss / (float)a.H + a.eps;
+    float f = 1.0f / sqrtf(t);
+    if (!mean_holds(t) || (a.out_dt == SEEDMM_I8 && !(top < INFINITY))) {   // (the whole workgroup)
+        const float top0 = top;
+        pass(nullptr);
+        if (top > 0.f && top < INFINITY) {
+            up = -ilogbf(top);
+            pass(&up);
+            f = scaled_factor(a, ss, up);
+        } else {
+            top = top0;
+        }
     }
-    ss = wave_sum(ss);
-    top = wave_max(bad ? INFINITY : top);
-    if ((threadIdx.x & 63) == 0) { red[0][threadIdx.x >> 6] = ss; red[1][threadIdx.x >> 6] = top; }
-    __syncthreads();
-    ss = red[0][0]; top = red[1][0];
-    for (int i = 1; i < 16; ++i) { ss += red[0][i]; top = fmaxf(top, red[1][i]); }
-    const RowFactor o = row_factor(a, ss, top);
+    const RowScale o = row_scale(a, f, top);
     if (a.out_dt == SEEDMM_I8 && threadIdx.x == 0) a.scale[n] = o.sc;
     for (int64_t h = threadIdx.x; h < a.H; h += 1024) {
         float r = load_el(a.x, a.x_dt, n * a.ldx + h);
         if (a.d) r += load_el(a.d, a.d_dt, n * a.ldd + h);
-        const float v = (a.w ? r * load_el(a.w, a.w_dt, h) : r) * o.f;
+        const float rs = ldexpf(r, up), v = (a.w ? rs * load_el(a.w, a.w_dt, h) : rs) * f;
         if (a.res) {
             if (a.x_dt == SEEDMM_F32) ((float*)a.res)[n * a.ldr + h] = r;
             else ((uint16_t*)a.res)[n * a.ldr + h] = f32_to_bf16(r);

@@ -5,7 +5,7 @@ import math
 
 import pytest
 
-from test_gpu_dense import block_case, check_route, gen, norm_tol, say, sm  # noqa: F401
+from test_gpu_dense import DT, block_case, check_norm, check_route, gen, norm_tol, say, sm  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +79,42 @@ def test_route_weights_of_tiny_sigmoids(sm, E, k):
     for dt in (torch.float32, torch.bfloat16):
         check_route(sm, lg.to(dt), k, "sigmoid")
         check_route(sm, lg.to(dt), k, "sigmoid", bias)
+
+
+@pytest.mark.parametrize("H", [1, 40, 2048, 7167, 16384, 30001, 40000])
+@pytest.mark.parametrize("x", ["bf16", "f32"])
+def test_add_norm_of_rows_whose_squares_leave_fp32(sm, x, H):
+    """Rows so small or so large that their squares are no fp32 numbers, with eps of 0, of
+    1e-6 and of their squares' size; next to ordinary rows, zeros, an infinity and a NaN."""
+    import torch
+    g = gen(63)
+    base = 1 + torch.rand(H, generator=g)
+    sign = torch.where(torch.rand(H, generator=g) < 0.5, -1.0, 1.0)
+    sizes = (1e-37, 1e-30, 1e-25, 1e-21, 1e-19, 1e-15, 1.0, 1e15, 1e18, 1e19, 1e25, 1e37)
+    rows = torch.stack([base * sign * c for c in sizes] + [torch.zeros(H), base, base]).to(DT[x])
+    rows[3, H // 2] = 1e-30            # far apart in one row
+    if H > 1:
+        rows[9, H // 3] = 1e-15
+    rows[-2, H - 1], rows[-1, 0] = math.inf, math.nan
+    N, good = len(rows), range(len(sizes))
+    w = (1 + 0.3 * torch.rand(H, generator=g)).to(torch.bfloat16)
+    d = (rows.float().nan_to_num(0, 0, 0) * 0.25).to(DT[x])
+    xd, wd, dd = rows.cuda(), w.cuda(), d.cuda()
+    for eps in (0.0, 1e-6, 1e-38, 1e30):
+        for delta, dc in ((None, None), (dd, d)):
+            for out in ("f32", "bf16", "i8"):
+                o, sc, res = sm.add_norm(xd, wd, delta=delta, eps=eps, out_dtype=DT[out])
+                torch.cuda.synchronize()
+                e32 = float(torch.tensor(eps, dtype=torch.float32))
+                for n in good:
+                    s = slice(n, n + 1)
+                    say(H, x, eps, out, n)
+                    check_norm(o[s], None if sc is None else sc[s], None if delta is None else res[s],
+                               rows[s], None if dc is None else dc[s], w, e32, out, x)
+                if out == "i8":
+                    assert math.isnan(float(sc[N - 1])) and math.isnan(float(sc[N - 2]))
+                    assert bool((o[N - 2:] == 0).all())
+                    if eps:
+                        assert bool((o[N - 3] == 0).all()) and float(sc[N - 3]) == 2.0 ** -126
+                elif eps:
+                    assert bool((o[N - 3] == 0).all())
