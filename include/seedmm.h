@@ -416,7 +416,7 @@ int seedmm_cache_stats(const seedmm_cache *cache, uint64_t out[5]);
  *   SEEDMM_I8), and y is rounded once.  The sums run in a fixed order that depends on the
  *   sizes and types only: the same call gives the same bits.  A row of x with an infinity or NaN gives a row of y
  *   without finite meaning and leaves the other rows alone.
- * Errors: SEEDMM_EINVAL (null pointer, M, K or N < 0 or above 2^30, another group,
+ * Errors: SEEDMM_EINVAL (null pointer, M, K or N < 0, M or K above 2^30, N above 2^30 - 64, another group,
  * K % group != 0, ldx < K, ldy < M, bad dtype, x_scale missing or given without
  * SEEDMM_I8), SEEDMM_EALIGN (weight, x or the workspace not 16-byte aligned, ldx not a
  * multiple of 16 bytes where N > 1, another pointer not aligned to its type),

@@ -1332,10 +1332,16 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
 }
 
 constexpr int kMaxDim = 1 << 30;   // row and column indices of a tile stay in 32 bits
+constexpr int kMaxTokens = kMaxDim - 64;   // and a row of token tiles in one launch
 
 size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 int launch_status() { return hipGetLastError() == hipSuccess ? SEEDMM_OK : SEEDMM_EHIP; }
+
+// HIP takes fewer than 2^32 threads of a grid in one dimension: larger calls are launched in
+// parts of this many, over rows or tokens.
+constexpr int64_t kLaunchThreads = 1 << 30;
+int64_t type_bytes(int dt) { return dt == SEEDMM_F32 ? 4 : dt == SEEDMM_BF16 ? 2 : 1; }
 
 template <int XT, bool SF32, int GROUP, int JN, int KW>
 void launch_q4_kw(const Q4Args& a, hipStream_t st) {
@@ -1351,6 +1357,18 @@ void launch_q4_kw(const Q4Args& a, hipStream_t st) {
     const int64_t tiles = ((int64_t)a.M + 15) / 16;
     hipLaunchKernelGGL((k_q4<XT, SF32, GROUP, JN, KW>), dim3((unsigned)((tiles + RW - 1) / RW)),
                        dim3(kQ4Waves * 64), lds, st, a, slab);
+}
+
+// the product's weight rows m0 .. m0 + rows - 1
+template <bool SF32, int GROUP>
+Q4Args weight_rows(Q4Args a, int64_t m0, int64_t rows) {
+    const int64_t g = m0 * (a.K / GROUP) * (SF32 ? 4 : 2);
+    a.w += m0 * (a.K / 8);
+    a.s = (const char*)a.s + g;
+    a.b = (const char*)a.b + g;
+    a.y = (char*)a.y + m0 * (a.y_bf16 ? 2 : 4);
+    a.M = (int)(rows < a.M - m0 ? rows : a.M - m0);
+    return a;
 }
 
 // The fewer row tiles, the more waves share one (us with 2, 4, 8 waves, one bf16 token:
@@ -1412,8 +1430,12 @@ template <int XT, bool SF32, int GROUP>
 void launch_q4_group(const Q4Args& a, const Q4Plan& p, void* ws, hipStream_t st) {
     constexpr int PL = XT == SEEDMM_F32 ? 3 : 1;
     if (!p.wide) {
-        if (a.N * PL <= 4) launch_q4_jn<XT, SF32, GROUP, 1>(a, st);
-        else launch_q4_jn<XT, SF32, GROUP, 4>(a, st);
+        constexpr int64_t rows = kLaunchThreads / (kQ4Waves * 64) * 16;   // a row tile a workgroup, or more
+        for (int64_t m0 = 0; m0 < a.M; m0 += rows) {
+            const Q4Args b = weight_rows<SF32, GROUP>(a, m0, rows);
+            if (a.N * PL <= 4) launch_q4_jn<XT, SF32, GROUP, 1>(b, st);
+            else launch_q4_jn<XT, SF32, GROUP, 4>(b, st);
+        }
         return;
     }
     uint16_t* xp = (uint16_t*)ws;
@@ -1423,12 +1445,18 @@ void launch_q4_group(const Q4Args& a, const Q4Plan& p, void* ws, hipStream_t st)
         hipLaunchKernelGGL((k_q4_rows<XT, GROUP>), dim3((unsigned)(blocks < 65536 ? blocks : 65536)),
                            dim3(256), 0, st, a, xp, xg, p.Kp, p.Gp);
     }
-    Q4Wide c = {a, xp, xg, p.S > 1 ? (float*)((char*)ws + p.part) : nullptr, p.Kp, p.Gp, p.ksplit, p.tn, p.tm};
-    const dim3 grid((unsigned)((int64_t)p.tn * p.tm), (unsigned)p.S);
-    if constexpr (PL == 3) hipLaunchKernelGGL((k_q4_wide<-1, PL, SF32, GROUP, 2, 2, 2>), grid, dim3(256), 0, st, c);
-    else if (p.two) hipLaunchKernelGGL((k_q4_wide<-1, PL, SF32, GROUP, 2, 4, 2>), grid, dim3(256), 0, st, c);
-    else if (p.laid) hipLaunchKernelGGL((k_q4_wide<-1, PL, SF32, GROUP, 1, 4, 3>), grid, dim3(256), 0, st, c);
-    else hipLaunchKernelGGL((k_q4_wide<XT, PL, SF32, GROUP, 1, 4, GROUP == 32 ? 2 : 3>), grid, dim3(256), 0, st, c);
+    const int64_t most = kLaunchThreads / 256 / p.tn;     // row tiles a launch (in parts: S = 1)
+    const int tms = (int)(p.tm <= most ? p.tm : most > 1 ? most : 1);
+    for (int64_t m0 = 0; m0 < a.M; m0 += (int64_t)tms * 128) {
+        const Q4Args b = weight_rows<SF32, GROUP>(a, m0, (int64_t)tms * 128);
+        const int tm = (b.M + 127) / 128;
+        Q4Wide c = {b, xp, xg, p.S > 1 ? (float*)((char*)ws + p.part) : nullptr, p.Kp, p.Gp, p.ksplit, p.tn, tm};
+        const dim3 grid((unsigned)((int64_t)p.tn * tm), (unsigned)p.S);
+        if constexpr (PL == 3) hipLaunchKernelGGL((k_q4_wide<-1, PL, SF32, GROUP, 2, 2, 2>), grid, dim3(256), 0, st, c);
+        else if (p.two) hipLaunchKernelGGL((k_q4_wide<-1, PL, SF32, GROUP, 2, 4, 2>), grid, dim3(256), 0, st, c);
+        else if (p.laid) hipLaunchKernelGGL((k_q4_wide<-1, PL, SF32, GROUP, 1, 4, 3>), grid, dim3(256), 0, st, c);
+        else hipLaunchKernelGGL((k_q4_wide<XT, PL, SF32, GROUP, 1, 4, GROUP == 32 ? 2 : 3>), grid, dim3(256), 0, st, c);
+    }
     if (p.S > 1) {
         const int64_t n = (int64_t)a.N * a.M, jb = (n + 255) / 256;
         hipLaunchKernelGGL(k_q4_join, dim3((unsigned)(jb < 65536 ? jb : 65536)), dim3(256), 0, st, a,
@@ -1444,7 +1472,7 @@ void launch_q4(const Q4Args& a, int group, const Q4Plan& p, void* ws, hipStream_
 }
 
 template <bool SIG, int LT>
-void launch_route(const RouteArgs& a, hipStream_t st) {
+void launch_route_part(const RouteArgs& a, hipStream_t st) {
     const dim3 grid((unsigned)((a.T - 1) / 4 + 1)), block(256);
     if (a.E <= 64) hipLaunchKernelGGL((k_route<1, SIG, LT>), grid, block, 0, st, a);
     else if (a.E <= 128) hipLaunchKernelGGL((k_route<2, SIG, LT>), grid, block, 0, st, a);
@@ -1455,11 +1483,39 @@ void launch_route(const RouteArgs& a, hipStream_t st) {
     else hipLaunchKernelGGL((k_route<64, SIG, LT>), grid, block, 0, st, a);
 }
 
+template <bool SIG, int LT>
+void launch_route(const RouteArgs& a, hipStream_t st) {
+    constexpr int64_t tokens = kLaunchThreads / 64;
+    for (int64_t t0 = 0; t0 < a.T; t0 += tokens) {
+        RouteArgs p = a;
+        p.lg = (const char*)a.lg + t0 * a.ldl * type_bytes(LT);
+        p.ids += t0 * a.k;
+        p.w += t0 * a.k;
+        p.T = (int)(a.T - t0 < tokens ? a.T - t0 : tokens);
+        launch_route_part<SIG, LT>(p, st);
+    }
+}
+
+// the rows from n0 that one launch takes with `threads` a row
+NormArgs norm_rows(NormArgs a, int64_t n0, int threads) {
+    const int64_t rows = kLaunchThreads / threads;
+    a.x = (const char*)a.x + n0 * a.ldx * type_bytes(a.x_dt);
+    if (a.d) a.d = (const char*)a.d + n0 * a.ldd * type_bytes(a.d_dt);
+    if (a.res) a.res = (char*)a.res + n0 * a.ldr * type_bytes(a.x_dt);
+    a.out = (char*)a.out + n0 * a.ldo * type_bytes(a.out_dt);
+    if (a.scale) a.scale += n0;
+    a.N = (int)(a.N - n0 < rows ? a.N - n0 : rows);
+    return a;
+}
+
 template <int TPR, int NP, int XT, int DT>
 void launch_norm_as(const NormArgs& a, hipStream_t st) {
     const int rows = TPR < 256 ? 256 / TPR : 1;
-    hipLaunchKernelGGL((k_add_norm<TPR, NP, XT, DT>), dim3((unsigned)((a.N - 1) / rows + 1)),
-                       dim3(TPR < 256 ? 256 : TPR), 0, st, a);
+    for (int64_t n0 = 0; n0 < a.N; n0 += kLaunchThreads / TPR) {
+        const NormArgs p = norm_rows(a, n0, TPR);
+        hipLaunchKernelGGL((k_add_norm<TPR, NP, XT, DT>), dim3((unsigned)((p.N - 1) / rows + 1)),
+                           dim3(TPR < 256 ? 256 : TPR), 0, st, p);
+    }
 }
 
 template <int XT, int DT>
@@ -1470,7 +1526,12 @@ void launch_norm(const NormArgs& a, hipStream_t st) {
     else if (a.H <= 8192) launch_norm_as<256, 4, XT, DT>(a, st);
     else if (a.H <= 16384) launch_norm_as<1024, 2, XT, DT>(a, st);
     else if (a.H <= 32768) launch_norm_as<1024, 4, XT, DT>(a, st);
-    else hipLaunchKernelGGL(k_add_norm_long, dim3((unsigned)a.N), dim3(1024), 0, st, a);
+    else {
+        for (int64_t n0 = 0; n0 < a.N; n0 += kLaunchThreads / 1024) {
+            const NormArgs p = norm_rows(a, n0, 1024);
+            hipLaunchKernelGGL(k_add_norm_long, dim3((unsigned)p.N), dim3(1024), 0, st, p);
+        }
+    }
 }
 
 bool float_type(int dt) { return dt == SEEDMM_F32 || dt == SEEDMM_BF16; }
@@ -1484,7 +1545,7 @@ int seedmm_q4_gemv(const uint32_t* weight, const void* scales, const void* biase
                    int y_dtype, int ldy, int M, int K, int N, void* workspace,
                    size_t workspace_bytes, void* hip_stream) {
     if (group != 32 && group != 64 && group != 128) return SEEDMM_EINVAL;
-    if (M < 0 || K < 0 || N < 0 || M > kMaxDim || K > kMaxDim || N > kMaxDim || K % group != 0 || ldx < K || ldy < M)
+    if (M < 0 || K < 0 || N < 0 || M > kMaxDim || K > kMaxDim || N > kMaxTokens || K % group != 0 || ldx < K || ldy < M)
         return SEEDMM_EINVAL;
     if (!float_type(s_dtype) || !float_type(y_dtype)) return SEEDMM_EINVAL;
     if (!float_type(x_dtype) && x_dtype != SEEDMM_I8) return SEEDMM_EINVAL;
@@ -1510,8 +1571,6 @@ int seedmm_q4_gemv(const uint32_t* weight, const void* scales, const void* biase
     const Q4Plan p = q4_plan(x_dtype, group, M, K, N);
     if (p.total && (!workspace || workspace_bytes < p.total)) return SEEDMM_EWORKSPACE;
     if (p.total && !aligned16(workspace)) return SEEDMM_EALIGN;
-    // one grid's workgroups are counted in 31 bits
-    if (p.wide && (int64_t)p.tn * p.tm > 0x7FFFFFFF) return SEEDMM_EINVAL;
     Q4Args a = {weight, scales, biases, x, x_scale, y, M, K, N, ldx, ldy, y_dtype == SEEDMM_BF16};
     const bool sf = s_dtype == SEEDMM_F32;
     if (x_dtype == SEEDMM_F32) sf ? launch_q4<SEEDMM_F32, true>(a, group, p, workspace, st) : launch_q4<SEEDMM_F32, false>(a, group, p, workspace, st);

@@ -5,7 +5,8 @@ import math
 
 import pytest
 
-from test_gpu_dense import DT, block_case, check_norm, check_route, gen, norm_tol, say, sm  # noqa: F401
+from test_gpu_dense import (DT, U, block_case, check_norm, check_route, gen, norm_tol, q4_bound,  # noqa: F401
+                            q4_ref, route_ref, say, sm)
 
 pytestmark = pytest.mark.gpu
 
@@ -118,3 +119,78 @@ def test_add_norm_of_rows_whose_squares_leave_fp32(sm, x, H):
                         assert bool((o[N - 3] == 0).all()) and float(sc[N - 3]) == 2.0 ** -126
                 elif eps:
                     assert bool((o[N - 3] == 0).all())
+
+
+# ---- more threads than HIP takes in one grid (2^32 in one dimension) --------------------
+
+def around(n, part):
+    """Indices at the start, the end and every multiple of `part`."""
+    import torch
+    at = set(range(min(4, n))) | set(range(max(0, n - 4), n))
+    for b in range(part, n, part):
+        at |= set(range(b - 2, min(b + 2, n)))
+    return torch.tensor(sorted(at))
+
+
+@pytest.mark.parametrize("N,H,threads", [(2 ** 26 + 9, 3, 64), (2 ** 24 + 7, 520, 256), (2 ** 20 + 3, 8193, 1024)])
+def test_norm_of_more_rows_than_a_grid(sm, N, H, threads):
+    import torch
+    say("norm", N, H)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(64)
+    x = torch.empty(N, H, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    w = torch.rand(H, generator=g, device="cuda") + 0.5
+    d = torch.empty(N, H, dtype=torch.bfloat16, device="cuda").normal_(generator=g) if H == 3 else None
+    o = torch.empty(N, H, dtype=torch.int8, device="cuda")
+    sc = torch.full((N,), -1.0, device="cuda")
+    at = around(N, 2 ** 30 // threads)
+    xv, dv = x[at.cuda()].cpu(), None if d is None else d[at.cuda()].cpu()
+    sm.add_norm(x, w, delta=d, out=o, scale=sc, residual=None if d is None else x)
+    torch.cuda.synchronize()
+    assert bool((sc > 0).all())
+    for i, n in enumerate(at.tolist()):
+        s = slice(i, i + 1)
+        check_norm(o[n:n + 1], sc[n:n + 1], None if d is None else x[n:n + 1], xv[s],
+                   None if d is None else dv[s], w.cpu(), 1e-6, "i8", "bf16")
+    if H == 3:
+        assert bool((o.abs().amax(dim=1) == 127).all())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_of_more_tokens_than_a_grid(sm, score):
+    import torch
+    T, E, k = 2 ** 26 + 5, 8, 2
+    say("route", T, E, k, score)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(65)
+    lg = torch.empty(T, E, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    ids = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+    w = torch.full((T, k), -1.0, device="cuda")
+    sm.route(lg, k, score=score, ids=ids, w=w)
+    torch.cuda.synchronize()
+    assert bool((ids >= 0).all()) and bool(((w.sum(dim=1) - 1).abs() < 1e-6).all())
+    at = around(T, 2 ** 24)
+    ri, rw = route_ref(lg[at.cuda()].float().cpu().numpy(), k, score, None)
+    assert (ids[at.cuda()].cpu().numpy() == ri).all()
+    assert (abs(w[at.cuda()].cpu().numpy() - rw) <= 64 * U * rw).all()      # (2 span + 16) u, span < 24
+
+
+@pytest.mark.parametrize("N,M,part", [(1, 2 ** 29 + 40, 2 ** 25), (65, 2 ** 28 + 200, 2 ** 28)])
+def test_q4_of_more_weight_rows_than_a_grid(sm, N, M, part):
+    """One token: in parts of 2^25 rows; 65 tokens (two tiles): of 2^21 tiles of 128 rows."""
+    import torch
+    K, group = 32, 32
+    say("q4", N, M, K)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(66)
+    w = torch.empty(M, K // 8, dtype=torch.int32, device="cuda").random_(-2 ** 31, 2 ** 31 - 1, generator=g)
+    sc = torch.empty(M, 1, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    bi = torch.empty(M, 1, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    x = torch.empty(N, K, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    y = torch.full((N, M), math.nan, dtype=torch.bfloat16, device="cuda")
+    sm.q4_gemv({"weight": w.view(torch.uint32), "scales": sc, "biases": bi}, x, M, K, group, y=y)
+    torch.cuda.synchronize()
+    assert all(bool(torch.isfinite(r).all()) for r in y)
+    at = around(M, part).cuda()
+    ref, S = q4_ref(w[at].cpu(), sc[at].cpu(), bi[at].cpu(), x.cpu(), None, group)
+    assert bool(((y[:, at].cpu().double() - ref).abs() <= q4_bound(ref, S, K, "bf16")).all())
