@@ -494,8 +494,8 @@ int seedmm_route(const void *logits, int l_dtype, int64_t ldl, const float *bias
  *   w: fp32[T][top_k] receive the routing (each may be NULL);
  *   workspace: device scratch of seedmm_moe_block_workspace_bytes(block, T) bytes; overlapping
  *   calls use different ones.  side: as for seedmm_moe_ex.
- * Errors: those of the four calls, before anything runs; r, delta, y, norm_weight and the
- * router's arrays 16-byte aligned.
+ * Errors: those of the four calls, before anything runs (but for SEEDMM_EHIP, of a launch that
+ * HIP refuses); r, delta, y, norm_weight and the router's arrays 16-byte aligned.
  */
 typedef struct seedmm_block {
     const void *norm_weight;         /* [H] or NULL                                   */

@@ -1654,7 +1654,7 @@ int seedmm_moe_block(const seedmm_block* block, void* r, int r_dtype, const void
                      int delta_dtype, float* y, int32_t* ids, float* w, int T, void* workspace,
                      size_t workspace_bytes, void* hip_stream, const seedmm_side* side) {
     size_t at[6];
-    if (!block || T < 0) return SEEDMM_EINVAL;
+    if (!block || T < 0 || T > kMaxTokens) return SEEDMM_EINVAL;
     const seedmm_block& b = *block;
     if (!block_layout(block, T, at)) return SEEDMM_EINVAL;
     // every check of the four calls before the first launch: the routed layer's and the

@@ -165,3 +165,11 @@ def test_binding_module_counts_arguments(sm):
     for f in (sm._binding.q4_gemv, sm._binding.add_norm, sm._binding.route):
         with pytest.raises(TypeError, match="arguments are needed"):
             f(None)
+
+
+def test_moe_block_refuses_too_many_tokens_before_its_first_launch(sm):
+    """The product takes 2^30 - 64 tokens; a block of more may not have added delta to r when
+    it says so (a launch would give -4 here)."""
+    b = make_block(sm, top_k=1, H=64, I=32)
+    for T in (1 << 30, (1 << 30) - 63):
+        assert run_block(sm, b, T=T, wsb=1 << 62) == -1
