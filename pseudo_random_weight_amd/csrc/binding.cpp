@@ -138,15 +138,25 @@ bool stream_of(PyObject* handle, int dev, void** st) {
     return !PyErr_Occurred();
 }
 
+// The interpreter's lock given up for a scope.  What may wait for the device (a launch, for
+// room in its queue; an allocation) runs so: the stream may be waiting for Python code itself.
+struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // The call, with the tensors' device current.
 template <typename F>
 bool call(int dev, const char* what, F f) {
     int status;
-    if (c10::hip::current_device() == dev) {
-        status = f();
-    } else {
-        c10::DeviceGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
-        status = f();
+    {
+        Unlocked u;
+        if (c10::hip::current_device() == dev) {
+            status = f();
+        } else {
+            c10::DeviceGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
+            status = f();
+        }
     }
     if (status == SEEDMM_OK) return true;
     PyObject* e = PyObject_CallFunction(error_class, "is", status, what);
@@ -216,6 +226,7 @@ bool q4_gemv(PyObject* const* a) {
         ws = t.data_ptr();
         bytes = t.nbytes();
     } else if ((bytes = q4_bytes_fn(x.code, (int)group, (int)M, (int)K, (int)x.n)) != 0) {
+        Unlocked u;
         own = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, dev));
         ws = own.data_ptr();
     }

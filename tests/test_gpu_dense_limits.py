@@ -194,3 +194,47 @@ def test_q4_of_more_weight_rows_than_a_grid(sm, N, M, part):
     at = around(M, part).cuda()
     ref, S = q4_ref(w[at].cpu(), sc[at].cpu(), bi[at].cpu(), x.cpu(), None, group)
     assert bool(((y[:, at].cpu().double() - ref).abs() <= q4_bound(ref, S, K, "bf16")).all())
+
+
+def test_calls_let_other_python_threads_run(sm, tmp_path):
+    """A call that waits (a launch can, for room in its queue) does not hold the interpreter:
+    the library's functions are replaced by one that waits, two seconds at most, for a flag
+    that another Python thread sets."""
+    import ctypes
+    import subprocess
+    import threading
+    import time
+
+    import torch
+    src, so = tmp_path / "wait.c", str(tmp_path / "wait.so")
+    src.write_text("#include <unistd.h>\nvolatile int flag;\nint wait_flag(void) {\n"
+                   "  for (int i = 0; i < 2000; ++i) { if (flag) return 0; usleep(1000); }\n"
+                   "  return -1;\n}\n")
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", so, str(src)], check=True)
+    lib = ctypes.CDLL(so)
+    flag = ctypes.c_int.in_dll(lib, "flag")
+    address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
+    names = ("seedmm_q4_gemv", "seedmm_q4_workspace_bytes", "seedmm_add_norm", "seedmm_route")
+    real = [address(getattr(sm.lib(), n)) for n in names]
+    wait = address(lib.wait_flag)
+    x = torch.zeros(2, 64, device="cuda")
+    mat = {"weight": torch.zeros(16 * 8, dtype=torch.int32, device="cuda").view(torch.uint32),
+           "scales": torch.zeros(16, device="cuda"), "biases": torch.zeros(16, device="cuda")}
+    calls = (lambda: sm.q4_gemv(mat, x, 16, 64), lambda: sm.add_norm(x), lambda: sm.route(x, 2))
+    for c in calls:
+        c()
+    torch.cuda.synchronize()
+
+    def later():
+        time.sleep(0.05)
+        flag.value = 1
+    sm._binding.init(wait, real[1], wait, wait, sm.SeedmmError)
+    try:
+        for c in calls:
+            flag.value = 0
+            t = threading.Thread(target=later)
+            t.start()
+            c()         # -1 of the wait would raise
+            t.join()
+    finally:
+        sm._binding.init(*real, sm.SeedmmError)
