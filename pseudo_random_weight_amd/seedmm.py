@@ -608,16 +608,32 @@ class ExpertCache:
 
 
 # ---- dense operators around the routed layer -----------------------------------------
-# Their arguments are checked and marshalled in the module _binding (csrc/binding.cpp).
+# Their arguments are checked and marshalled in the module _binding (csrc/binding.cpp).  It is
+# built against the installed torch and loaded by the first call that needs it, so that the
+# calls above work without it.
 
-if not os.path.exists(os.path.join(_HERE, "_binding.so")):
-    raise ImportError(f"{os.path.join(_HERE, '_binding.so')} is missing: build it with "
-                      "`python -m pseudo_random_weight_amd.build`")
-from . import _binding  # noqa: E402
+_dense = None      # the module, once loaded
 
-_binding.init(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value
-                for n in ("seedmm_q4_gemv", "seedmm_q4_workspace_bytes", "seedmm_add_norm",
-                          "seedmm_route")), SeedmmError)
+
+def _load_binding():
+    global _dense
+    path = os.path.join(_HERE, "_binding.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it with "
+                          "`python -m pseudo_random_weight_amd.build`")
+    from . import _binding as m
+    m.init(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value
+             for n in ("seedmm_q4_gemv", "seedmm_q4_workspace_bytes", "seedmm_add_norm",
+                       "seedmm_route")), SeedmmError)
+    _dense = m
+    return m
+
+
+def __getattr__(name):
+    if name == "_binding":
+        return _dense or _load_binding()
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
 
 _FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
 _ROWS = {torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8}
@@ -687,8 +703,8 @@ def q4_gemv(mat: dict, x: torch.Tensor, M: int, K: int, group: int = 64, x_scale
                 with _on(stream):
                     workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
         stream = _handle(stream, x)
-    _binding.q4_gemv(mat["weight"], mat["scales"], mat["biases"], group, x, x_scale, y, workspace,
-                     M, K, stream)
+    (_dense or _load_binding()).q4_gemv(mat["weight"], mat["scales"], mat["biases"], group, x,
+                                        x_scale, y, workspace, M, K, stream)
     return y
 
 
@@ -709,8 +725,8 @@ def add_norm(x: torch.Tensor, weight=None, delta=None, eps: float = 1e-6,
     if delta is not None and residual is None:
         with _on(stream):
             residual = torch.empty(_gpu(x, "x").shape, dtype=x.dtype, device=x.device)
-    _binding.add_norm(x, weight, delta, eps, residual, out, scale,
-                      None if stream is None else _handle(stream, _gpu(x, "x")))
+    (_dense or _load_binding()).add_norm(x, weight, delta, eps, residual, out, scale,
+                                         None if stream is None else _handle(stream, _gpu(x, "x")))
     return out, scale, x if residual is None else residual
 
 
@@ -734,8 +750,8 @@ def route(logits: torch.Tensor, top_k: int, bias=None, score: str = "softmax", i
                 ids = torch.empty(shape, dtype=torch.int32, device=logits.device)
             if w is None:
                 w = torch.empty(shape, dtype=torch.float32, device=logits.device)
-    _binding.route(logits, top_k, bias, kind, ids, w,
-                   None if stream is None else _handle(stream, _gpu(logits, "logits")))
+    (_dense or _load_binding()).route(logits, top_k, bias, kind, ids, w,
+                                      None if stream is None else _handle(stream, _gpu(logits, "logits")))
     return ids, w
 
 

@@ -173,3 +173,41 @@ def test_moe_block_refuses_too_many_tokens_before_its_first_launch(sm):
     b = make_block(sm, top_k=1, H=64, I=32)
     for T in (1 << 30, (1 << 30) - 63):
         assert run_block(sm, b, T=T, wsb=1 << 62) == -1
+
+
+def test_the_library_imports_without_the_dense_binding(tmp_path):
+    """Callers of the seed-coded products need libseedmm.so alone: a package without _binding.so
+    (or with one that another torch was built for) imports, answers, and names the file at
+    the first dense call."""
+    import os
+    import subprocess
+    import sys
+
+    import pseudo_random_weight_amd as pkg
+    here, there = os.path.dirname(pkg.__file__), tmp_path / "pseudo_random_weight_amd"
+    there.mkdir()
+    for f in os.listdir(here):
+        if f.endswith(".py") or f == "libseedmm.so":
+            os.symlink(os.path.join(here, f), there / f)
+    code = """
+import torch
+from pseudo_random_weight_amd import seedmm as sm
+assert sm.moe_workspace_bytes(4, 2, 8, 64, 32) > 0 and sm.q4_workspace_bytes(torch.float32, 64, 100, 2048, 6) > 0
+x = torch.zeros(2, 8)
+for call in (lambda: sm.route(x, 2, ids=x, w=x), lambda: sm.add_norm(x, out=x), lambda: sm._binding,
+             lambda: sm.q4_gemv({"weight": x, "scales": x, "biases": x}, x, 16, 64, y=x)):
+    try:
+        call()
+    except ImportError as e:
+        assert "_binding" in str(e)
+    else:
+        raise SystemExit("a dense call without its module")
+print("imported")
+"""
+    run = [sys.executable, "-c", code]
+    env = dict(os.environ, PYTHONPATH=str(tmp_path))
+    for text in (None, b"no library"):
+        if text:
+            (there / "_binding.so").write_bytes(text)
+        res = subprocess.run(run, cwd=tmp_path, env=env, capture_output=True, text=True, timeout=300)
+        assert "imported" in res.stdout, res.stderr
