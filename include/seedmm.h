@@ -412,26 +412,31 @@ int seedmm_cache_stats(const seedmm_cache *cache, uint64_t out[5]);
  *   y: [N][ldy] of y_dtype (SEEDMM_F32 or SEEDMM_BF16), overwritten; columns M .. ldy - 1
  *   are left as they were.
  *   Weights are not rounded to the activations' type: the codes enter the matrix
- *   instructions as integers, products are exact, sums are fp32 (int32 inside a group for
- *   SEEDMM_I8), and y is rounded once.  The sums run in a fixed order that depends on the
- *   sizes and types only: the same call gives the same bits.  A row of x with an infinity or NaN gives a row of y
- *   without finite meaning and leaves the other rows alone.
- * Errors: SEEDMM_EINVAL (null pointer, M, K or N < 0, M or K above 2^30, N above 2^30 - 64, another group,
- * K % group != 0, ldx < K, ldy < M, bad dtype, x_scale missing or given without
+ *   instructions as integers, code times activation is exact, sums are fp32 (exact inside a
+ *   group for SEEDMM_I8), the scales and biases multiply the groups' sums in fp32 (with fp32
+ *   biases and laid-out rows a group's b X is off by less than 2^-21 of it), and y is
+ *   rounded once.  15 sum_{k in g} |x[n][k]| of a group has to be an fp32 number, and what an
+ *   fp32 x has below 2^-133 is dropped.  The sums run in a fixed order that depends on the
+ *   sizes and types only: the same call gives the same bits.  A row of x with an infinity or
+ *   NaN gives a row of y without finite meaning and
+ *   leaves the other rows alone.
+ * Errors: SEEDMM_EINVAL (null pointer, M, K or N < 0, M or K above 2^30, N above 2^30 - 64,
+ * another group, K % group != 0, ldx < K, ldy < M, bad dtype, x_scale missing or given without
  * SEEDMM_I8), SEEDMM_EALIGN (weight, x or the workspace not 16-byte aligned, ldx not a
  * multiple of 16 bytes where N > 1, another pointer not aligned to its type),
- * SEEDMM_EWORKSPACE (workspace missing or smaller than seedmm_q4_workspace_bytes), SEEDMM_EHIP.  M = 0 or
- * N = 0 is an empty success; K = 0 writes zeros.
+ * SEEDMM_EWORKSPACE (workspace missing or smaller than seedmm_q4_workspace_bytes),
+ * SEEDMM_EHIP.  M = 0 or N = 0 is an empty success; K = 0 writes zeros.
  */
 int seedmm_q4_gemv(const uint32_t *weight, const void *scales, const void *biases, int s_dtype,
                    int group, const void *x, int x_dtype, int ldx, const float *x_scale, void *y,
                    int y_dtype, int ldy, int M, int K, int N, void *workspace,
                    size_t workspace_bytes, void *hip_stream);
 /* Bytes of device scratch (16-byte aligned, contents need not be initialised) that a product
- * of these sizes needs: 0 for few rows (up to 16; 5 with fp32 x), where workspace may be
- * NULL; else the activation rows in the operands' order and, where K is split over
- * workgroups, the partial sums.  0 on bad arguments.  Calls that overlap in time use
- * different workspaces. */
+ * of these sizes needs: 0 for few rows (up to 16; 5 with fp32 x); else the activation rows in
+ * the operands' order, where a launch lays them out (fp32 x, and large products), and the
+ * partial sums, where K is split over workgroups; 0 too where neither is so.  Where it is 0,
+ * workspace may be NULL.  0 on bad arguments.  Calls that overlap in time use different
+ * workspaces. */
 size_t seedmm_q4_workspace_bytes(int x_dtype, int group, int M, int K, int N);
 
 /*

@@ -23,13 +23,13 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float f) { return __builtin_bit_
 // seedmm_q4_gemv.  y[n][m] = sx[n] sum_g ( s[m][g] D[m][g][n] + b[m][g] X[g][n] ) with
 // D = sum of q x over the group's columns and X = sum of x.
 //
-// Both sums are exact products: a code q is an integer of 4 bits, so it enters the matrix
+// Products q x are exact: a code q is an integer of 4 bits, so it enters the matrix
 // instruction without rounding, and the scale multiplies the group's fp32 sum afterwards
 // (a weight s q + b is never rounded to the activation's type).
 //   bf16 x: a code is an integer below 16, exact in bf16.
 //   fp32 x: split into three bf16 of 8 bits each (truncated, so the split is exact), three
-//     rows of the same instruction.
-//   int8 x: the integer instruction; D is exact.
+//     rows of the same instruction (few tokens), or three instructions (many).
+//   int8 x: the integer instruction (few tokens), or exact bf16 (many); D is exact.
 // ----------------------------------------------------------------------------------
 constexpr int kQ4Waves = 8;      // of a workgroup for a few tokens
 
@@ -382,11 +382,13 @@ __global__ __launch_bounds__(kQ4Waves * 64) void k_q4(const Q4Args a, int slab) 
 
 // Many tokens.  k_q4_rows writes the activations once as bf16 rows in the operands' order
 // (fp32: three planes) and the groups' sums as three bf16 planes; k_q4_wide multiplies tiles
-// of them with the codes on 32x32x16 instructions.
+// of them with the codes on 32x32x16 instructions.  In products with little to lay out it
+// takes the rows as they are (RAW), with no launch before it.
 //
-// The bias term is a product of its own over the groups, sum_g b[m][g] X[n][g]: it starts
-// the accumulators with matrix instructions (3 for 16 groups; 6 with fp32 biases, which
-// are split as well), so the vector units only add s D, one fma an element a 64 columns.
+// With laid-out rows the bias term is a product of its own over the groups, sum_g b[m][g]
+// X[n][g]: it starts the accumulators with matrix instructions (3 for 16 groups; 6 with fp32
+// biases, which are split as well: of the nine products of parts those of 2^-22 and less of
+// the term are left out), so the vector units only add s D, one fma an element a 64 columns.
 //
 // A workgroup takes 128 weight rows by 32 TT tokens, a wave 32 of the rows.  Lane r + 32 h loads the
 // 16 bytes of row r that hold columns 32 h .. 32 h + 31 of a 64-column step: word j is its

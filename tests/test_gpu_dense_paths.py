@@ -172,3 +172,19 @@ def test_large_products_at_once(sm):
     for t in threads:
         t.join()
     assert not bad, bad
+
+
+@pytest.mark.parametrize("x,N,M,K", [("f32", 3, 100, 256), ("f32", 40, 100, 256), ("bf16", 3, 100, 256),
+                                     ("bf16", 40, 100, 256), ("bf16", 70, 8200, 4224)])
+def test_activations_of_few_bits_stay_exact_down_to_2_to_the_minus_133(sm, x, N, M, K):
+    """The exact inputs times 2^-90 .. 2^-130 (subnormal ones among them), scales times 2^60."""
+    import torch
+    case = exact_case(N, M, K, 64, x, "f32", "x", 5)
+    ref = exact_result(*(None if t is None else t.cuda() for t in case), 64)
+    mat = put(case[0], case[1] * 2.0 ** 60, case[2] * 2.0 ** 60)
+    for e in (-90, -110, -126, -130):
+        xv = (case[3].double() * 2.0 ** e).to(case[3].dtype)
+        assert bool((xv.double() == case[3].double() * 2.0 ** e).all())
+        got = sm.q4_gemv(mat, xv.cuda(), M, K, 64)
+        torch.cuda.synchronize()
+        assert bool((got.double() == ref * 2.0 ** (60 + e)).all()), e
