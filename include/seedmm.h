@@ -418,8 +418,7 @@ int seedmm_cache_stats(const seedmm_cache *cache, uint64_t out[5]);
  *   rounded once.  15 sum_{k in g} |x[n][k]| of a group has to be an fp32 number, and what an
  *   fp32 x has below 2^-133 is dropped.  The sums run in a fixed order that depends on the
  *   sizes and types only: the same call gives the same bits.  A row of x with an infinity or
- *   NaN gives a row of y without finite meaning and
- *   leaves the other rows alone.
+ *   NaN gives a row of y without finite meaning and leaves the other rows alone.
  * Errors: SEEDMM_EINVAL (null pointer, M, K or N < 0, M or K above 2^30, N above 2^30 - 64,
  * another group, K % group != 0, ldx < K, ldy < M, bad dtype, x_scale missing or given without
  * SEEDMM_I8), SEEDMM_EALIGN (weight, x or the workspace not 16-byte aligned, ldx not a
@@ -445,7 +444,8 @@ size_t seedmm_q4_workspace_bytes(int x_dtype, int group, int M, int K, int N);
  *     r = x + delta;   out = r / sqrt(mean_h r^2 + eps) * weight
  *   x: [N][ldx] fp32 or bf16;  delta: [N][ldd] fp32 or bf16, or NULL (r = x);
  *   weight: [H] fp32 or bf16, or NULL (ones);
- *   residual: [N][ldr] of x's type receiving r, or NULL; it may be x itself (same ld).
+ *   residual: [N][ldr] of x's type receiving r, or NULL; it may be x itself, with ldr = ldx.
+ *   Outputs overlap inputs in no other way.
  *   out: [N][ldo] of out_dtype.  SEEDMM_F32, SEEDMM_BF16: the value, rounded once.
  *   SEEDMM_I8: codes round(value / scale[n]) in [-127, 127] with scale[n] = max_h |value| /
  *   127 (at least 2^-126); a row that holds an infinity or NaN gets scale NaN and codes 0.
@@ -456,8 +456,8 @@ size_t seedmm_q4_workspace_bytes(int x_dtype, int group, int M, int K, int N);
  *   and a row of zeros with eps = 0 has no value (0/0).  Rows of any ld
  *   and alignment are taken; rows that start on 16 bytes are faster.  Elements past H are
  *   left as they were.
- * Errors: SEEDMM_EINVAL (null pointer, N or H < 0, ld < H, bad dtype, eps negative or not
- * finite, scale missing or given without SEEDMM_I8), SEEDMM_EALIGN (a pointer not aligned
+ * Errors: SEEDMM_EINVAL (null pointer, N or H < 0, ld < H, x as residual with another ld, bad
+ * dtype, eps negative or not finite, scale missing or given without SEEDMM_I8), SEEDMM_EALIGN (a pointer not aligned
  * to its type), SEEDMM_EHIP.  N = 0 or H = 0 is an empty success.
  */
 int seedmm_add_norm(const void *x, int x_dtype, int64_t ldx, const void *delta, int delta_dtype,

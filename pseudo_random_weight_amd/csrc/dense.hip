@@ -1596,6 +1596,7 @@ int seedmm_add_norm(const void* x, int x_dtype, int64_t ldx, const void* delta, 
         return SEEDMM_EINVAL;
     if (!float_type(out_dtype) && out_dtype != SEEDMM_I8) return SEEDMM_EINVAL;
     if (ldx < H || (delta && ldd < H) || (residual && ldr < H) || ldo < H) return SEEDMM_EINVAL;
+    if (residual && residual == x && ldr != ldx && N > 1) return SEEDMM_EINVAL;   // rows over others' rows
     if ((out_dtype == SEEDMM_I8) != (scale != nullptr) && N > 0 && H > 0) return SEEDMM_EINVAL;
     if (N == 0 || H == 0) return SEEDMM_OK;
     if (!x || !out) return SEEDMM_EINVAL;

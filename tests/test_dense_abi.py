@@ -211,3 +211,13 @@ print("imported")
             (there / "_binding.so").write_bytes(text)
         res = subprocess.run(run, cwd=tmp_path, env=env, capture_output=True, text=True, timeout=300)
         assert "imported" in res.stdout, res.stderr
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(ldr=72), -1), (dict(ldx=72), -1), (dict(ldx=72, ldr=72, d=F + 1, dd=F32), -2),
+    (dict(ldr=72, N=1, d=F + 1), -2), (dict(ldr=72, res=F + 0x1000, d=F + 1), -2),
+])
+def test_add_norm_in_place_takes_one_row_stride(sm, kw, expect):
+    """x as residual with another row stride would write rows that others still read.  (-2, of
+    a misaligned delta, stands for a call that passes this check.)"""
+    assert norm(sm, **kw) == expect
