@@ -802,7 +802,7 @@ __device__ __forceinline__ uint32_t wave_umin(uint32_t v) {
 // scale is max |r w| times the row's factor over 127: one pass finds both statistics, and
 // a row stays in registers between its load and its store (rows up to 32,768 elements;
 // longer ones are read twice).  A row whose mean square fp32 does not hold is multiplied by
-// a power of two, exactly, and summed again (asking for it costs 0.07 us of 2.6 at one token
+// a power of two, exactly, and summed again (asking for it costs 0.08 us of 2.6 at one token
 // and nothing that shows at 4096 x 2048).
 // ----------------------------------------------------------------------------------
 struct NormArgs {
@@ -961,7 +961,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_add_norm(const NormAr
         }
         if (a.res && cnt[p] > 0) store8<XT>(a.res, n * a.ldr + (p * TPR + tid) * 8, cnt[p], r[p]);
     }
-    auto weighted = [&]() {     // max |r w| of this thread; infinite where one is not finite
+    auto weighted = [&]() __attribute__((always_inline)) {     // max |r w| of this thread; infinite where one is not finite
         float m = 0.f;
         bool bad = false;
 #pragma unroll
@@ -974,7 +974,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_add_norm(const NormAr
             }
         return bad ? INFINITY : m;
     };
-    auto row_stats = [&]() {    // both statistics over the row's threads
+    auto row_stats = [&]() __attribute__((always_inline)) {    // both statistics over the row's threads
         ss = wave_sum(ss);
         if (a.out_dt == SEEDMM_I8) top = wave_max(top);
         if constexpr (NW > 1) {
