@@ -217,7 +217,7 @@ __device__ __forceinline__ float place8_as_bf16(const Raw8<SEEDMM_I8>& x, char* 
 // cache lines, and the wave's own piece of LDS hands them to the lanes that multiply them
 // (each lane loading its own 16 bytes, 64 bytes a row, took 54 us for 131072 x 2048 at one
 // token against 30 us: the texture path passes one line at a time).  That size streams
-// its 152 MB at 5.2 TB/s with 3 sets of inputs in turn, 4.3 with 8; small matrices are bound by the
+// its 152 MB at 5.2 TB/s with 3 sets of inputs in turn, 4.5 with 8; small matrices are bound by the
 // latency of one launch and two dependent loads (100 x 2048: 3.4 us, 2048 x 2048: 3.5 us).
 // The D tile of 16x16x32 instructions has a row a token: up to 4 activation rows sit in D
 // rows 0, 4, 8, 12 (JN = 1), so each lane scales one value a group instead of four.
@@ -1401,9 +1401,9 @@ Q4Plan q4_plan(int x_dtype, int group, int M, int K, int N) {
     p.Kp = (K + 255) / 256 * 256;
     p.Gp = (K / group + 15) / 16 * 16;
     // Tiles of 64 tokens by 128 weight rows where they make 512 workgroups (two a CU);
-    // else of 32 by 128 with K split until they do (256 x 8192 x 2048: 26 us against 31;
-    // 61 x 5125 x 4160: one split 73 us, seven 24 us; as first built).  fp32 rows are three
-    // planes of work: always 64.
+    // else of 32 by 128 with K split until they do (us by this rule, with tiles of 64 and K
+    // split, with one split of K: 256 x 8192 x 2048 24.0 33.5 24.2, 61 x 5125 x 4160 19.9 23.0
+    // 37.9, 64 x 8192 x 8192 31.1 31.6 49.5).  fp32 rows are three planes of work: always 64.
     const int64_t tm = ((int64_t)M + 127) / 128;
     p.two = PL == 3 || (((int64_t)N + 63) / 64) * tm >= 512;
     const int BT = p.two ? 64 : 32, slab = PL == 3 ? 128 : 256;
