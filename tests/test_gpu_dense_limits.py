@@ -238,3 +238,25 @@ def test_calls_let_other_python_threads_run(sm, tmp_path):
             t.join()
     finally:
         sm._binding.init(*real, sm.SeedmmError)
+
+
+def test_a_refused_scratch_allocation_is_torch_s_out_of_memory(sm):
+    """As where the caller's own allocations fail; the next call works."""
+    import torch
+    N, M, K = 2 ** 20, 1, 32            # 1.6 GB of laid-out fp32 rows
+    torch.cuda.empty_cache()
+    x = torch.ones(N, K, device="cuda")
+    mat = {"weight": torch.full((4,), 0x11111111, dtype=torch.int32, device="cuda").view(torch.uint32),
+           "scales": torch.ones(1, device="cuda"), "biases": torch.zeros(1, device="cuda")}
+    y = torch.empty(N, M, device="cuda")
+    assert sm.q4_workspace_bytes(torch.float32, 32, M, K, N) > 2 ** 30
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + 2 ** 29) / total)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            sm.q4_gemv(mat, x, M, K, 32, y=y)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    sm.q4_gemv(mat, x, M, K, 32, y=y)
+    torch.cuda.synchronize()
+    assert bool((y == 32).all())
