@@ -519,6 +519,141 @@ int seedmm_moe_block(const seedmm_block *block, void *r, int r_dtype, const void
                      int delta_dtype, float *y, int32_t *ids, float *w, int T, void *workspace,
                      size_t workspace_bytes, void *hip_stream, const seedmm_side *side);
 
+/*
+ * Routed experts in 8-bit integers.  Not every expert of a pack is a seed (K2-Horizon card,
+ * "This upload": 64 value experts, top 4, and the dense layers stay affine): these operators
+ * serve the ones that are kept as 8-bit integers with a scale a channel.  seedmm_moe_sort puts
+ * a routed batch's rows in the order of their experts, seedmm_i8_gemv multiplies each run of
+ * rows with its expert's matrix, seedmm_swiglu joins gate and up, seedmm_moe_unsort returns
+ * the weighted sum of each token's rows, and seedmm_moe_i8 is the routed layer made of them.
+ * Rows of any leading dimension and alignment (of their type) are taken; rows that start on 16
+ * bytes are faster.  No result depends on the order in which anything runs: the same call
+ * gives the same bits, and a token's result does not depend on the batch around it.
+ *
+ * seedmm_i8_gemv -- Y[n] = W X[n] for N rows of 8-bit integers with a scale a row, W in 8-bit
+ * integers with a scale a channel, for one matrix or one an expert:
+ *     y[n][m] = ( sum_k x[n][k] weight[e][m][k] ) * x_scale[n] * scales[e][m]
+ *   weight: int8[E][M][K];  scales: [E][M] of s_dtype (SEEDMM_F32 or SEEDMM_BF16);
+ *   offsets: NULL (E = 1, all rows), or device int32[E + 1], not decreasing, from 0 to at most
+ *   N: rows offsets[e] .. offsets[e + 1] - 1 belong to expert e (seedmm_moe_sort writes them).
+ *   Rows of y from offsets[E] on are left as they were.  Values outside of [0, N] are taken as
+ *   the nearer end, so a wrong array gives wrong rows, never an access outside of x and y.
+ *   x: int8 [N][ldx];  x_scale: fp32[N];  y: [N][ldy] of y_dtype (SEEDMM_F32, SEEDMM_BF16),
+ *   overwritten; columns M .. ldy - 1 are left as they were.
+ *   The sums are exact (int32; all 256 codes); one is converted to fp32, multiplied by the row's
+ *   scale and then by the channel's, each rounded to fp32, and y rounded once: sum * x_scale
+ *   has to be an fp32 number.  A scale of NaN gives a row or a column of NaN.
+ * Errors: SEEDMM_EINVAL (null pointer, M, K or N < 0, M or N above 2^30, K above 131,071 (the
+ * sums would leave int32), E outside [1, 4096], E != 1 without offsets, ldx < K, ldy < M, bad dtype),
+ * SEEDMM_EALIGN (a pointer not aligned to its type), SEEDMM_EHIP.  M = 0 or N = 0 is an empty
+ * success; with K = 0 the sums are 0 (weight and x may be NULL).
+ */
+int seedmm_i8_gemv(const int8_t *weight, const void *scales, int s_dtype, int E,
+                   const int32_t *offsets, const int8_t *x, int64_t ldx, const float *x_scale,
+                   void *y, int y_dtype, int64_t ldy, int M, int K, int N, void *hip_stream);
+
+/*
+ * seedmm_moe_sort -- the rows of a routed batch in the order of their experts (the grouping
+ * of seedmm_moe_dispatch as rows in memory).  Pair p = t*top_k + s is token t's slot s:
+ *     the pairs with topk_ids[p] in [0, E) are ordered by (topk_ids[p], p);
+ *     inverse[p] = the pair's place in that order, or -1 for any other id;
+ *     offsets[e] = number of pairs with an id in [0, e), e = 0 .. E;
+ *     rows[inverse[p]] = x[t],  row_scale[inverse[p]] = x_scale[t].
+ *   topk_ids: int32[T][top_k]; an id outside of [0, E) drops its slot (an expert of another
+ *   device, a padding token); a token may name an expert twice.
+ *   x: [T][ldx] of x_dtype (SEEDMM_F32, SEEDMM_BF16 or SEEDMM_I8);  x_scale: fp32[T] or NULL;
+ *   rows: [T*top_k][ldr] of x_dtype; rows from offsets[E] on and columns H .. ldr - 1 are left
+ *   as they were;  row_scale: fp32[T*top_k], given with x_scale;  offsets: int32[E + 1];
+ *   inverse: int32[T][top_k].  H = 0 writes the order alone (x and rows may be NULL).
+ *   The gradient of rows with respect to x is seedmm_moe_unsort without weights.
+ *   workspace: device scratch of seedmm_moe_sort_workspace_bytes(T, top_k, E) bytes, 16-byte
+ *   aligned, contents need not be initialised; NULL where that is 0 (small batches).  Calls
+ *   that overlap in time use different ones.
+ * Errors: SEEDMM_EINVAL (null pointer, T or H < 0, H above 2^30, top_k outside [1, 64], T*top_k >= 2^31, E
+ * outside [1, 4096], ldx or ldr < H, bad dtype, one scale without the other), SEEDMM_EALIGN (a
+ * pointer not aligned to its type), SEEDMM_EWORKSPACE, SEEDMM_EHIP.  T = 0 writes offsets of 0.
+ */
+int seedmm_moe_sort(const int32_t *topk_ids, int T, int top_k, int E, const void *x, int x_dtype,
+                    int64_t ldx, const float *x_scale, void *rows, int64_t ldr, float *row_scale,
+                    int H, int32_t *offsets, int32_t *inverse, void *workspace,
+                    size_t workspace_bytes, void *hip_stream);
+size_t seedmm_moe_sort_workspace_bytes(int T, int top_k, int E);
+
+/*
+ * seedmm_moe_unsort -- sorted rows back to their tokens, weighted and summed:
+ *     y[t] = sum_s topk_w[t][s] * rows[inverse[t][s]]   over the slots with a row
+ *   rows: [n_rows][ldr] of r_dtype (SEEDMM_F32 or SEEDMM_BF16);  inverse: int32[T][top_k] of
+ *   seedmm_moe_sort; a value outside of [0, n_rows) is a slot without a row: neither a row nor
+ *   its weight enters;  topk_w: fp32[T][top_k], or NULL (ones: the gradient of seedmm_moe_sort);
+ *   y: [T][ldy] of y_dtype (SEEDMM_F32 or SEEDMM_BF16), overwritten (0 for a token without
+ *   rows); columns H .. ldy - 1 are left as they were.
+ *   Summed in fp32 in slot order, rounded once.
+ * seedmm_moe_unsort_grad -- its gradients for dy = d loss / d y (what a routed expert's row and
+ * its weight mean to a loss; the experts that matter most are the ones to keep in more bits):
+ *     drows[inverse[t][s]] = topk_w[t][s] * dy[t];   dw[t][s] = sum_h dy[t][h] rows[inverse[t][s]][h]
+ *   dy: [T][ldd] fp32 or bf16;  drows: [n_rows][ldg] of r_dtype, or NULL; rows that no slot
+ *   names are left as they were;  dw: fp32[T][top_k], 0 for slots without a row, or NULL (rows
+ *   may then be NULL).  Sums in fp32 in a fixed order; no atomics.  The inverse names each row
+ *   at most once.  drows may be rows itself with ldg = ldr; outputs overlap inputs in no other
+ *   way.
+ * Errors: SEEDMM_EINVAL (null pointer, T, H or n_rows < 0, H above 2^30, top_k outside [1, 64],
+ * T*top_k >= 2^31, a leading dimension < H, bad dtype, rows as drows with another ld), SEEDMM_EALIGN (a pointer not aligned to its type), SEEDMM_EHIP.  T = 0 is an empty
+ * success, and so is H = 0 but for dw, which is then 0.
+ */
+int seedmm_moe_unsort(const void *rows, int r_dtype, int64_t ldr, int n_rows,
+                      const int32_t *inverse, const float *topk_w, void *y, int y_dtype,
+                      int64_t ldy, int T, int top_k, int H, void *hip_stream);
+int seedmm_moe_unsort_grad(const void *dy, int dy_dtype, int64_t ldd, const void *rows, int r_dtype,
+                           int64_t ldr, int n_rows, const int32_t *inverse, const float *topk_w,
+                           void *drows, int64_t ldg, float *dw, int T, int top_k, int H,
+                           void *hip_stream);
+
+/*
+ * seedmm_swiglu -- h = silu(gate) * up of the rows of a gate-and-up product (the SwiGLU of
+ * seedmm_moe as an operator of its own), in a float type or as rows for the next product:
+ *     h[n][i] = g / (1 + exp(-g)) * u,  g = gate_up[n][i],  u = gate_up[n][I + i]
+ *   gate_up: [N][ldg] of g_dtype (SEEDMM_F32 or SEEDMM_BF16), ldg >= 2 I;
+ *   out: [N][ldo] of out_dtype.  SEEDMM_F32, SEEDMM_BF16: h, computed in fp32, rounded once.
+ *   SEEDMM_I8: codes round(h / scale[n]) in [-127, 127] with scale[n] = max_i |h| / 127 (at
+ *   least 2^-126); a row that holds an infinity or NaN gets scale NaN and codes 0 (as
+ *   seedmm_add_norm's).  scale: fp32[N] with SEEDMM_I8, NULL otherwise.
+ *   count: NULL, or device int32[1]: only the first count[0] rows exist (the offsets[E] of
+ *   seedmm_moe_sort); rows and scales behind are left as they were and not read.
+ * Errors: SEEDMM_EINVAL (null pointer, N or I < 0, I above 2^29, ldg < 2 I, ldo < I, bad dtype,
+ * scale missing or given without SEEDMM_I8), SEEDMM_EALIGN (a pointer not aligned to its type),
+ * SEEDMM_EHIP.  N = 0 or I = 0 is an empty success.
+ */
+int seedmm_swiglu(const void *gate_up, int g_dtype, int64_t ldg, void *out, int out_dtype,
+                  int64_t ldo, float *scale, const int32_t *count, int N, int I, void *hip_stream);
+
+/*
+ * seedmm_moe_i8 -- one routed layer of SwiGLU experts in 8-bit integers:
+ *     y[t] = sum_s topk_w[t][s] * down_e h,  h = i8( silu(gate_e x[t]) * (up_e x[t]) ),
+ *     e = topk_ids[t][s]
+ *   by seedmm_moe_sort, seedmm_i8_gemv (gate and up at once, bf16 rows), seedmm_swiglu (8-bit
+ *   rows), seedmm_i8_gemv (bf16 rows) and seedmm_moe_unsort, with their results: an id outside
+ *   of [0, E) drops its slot, a token without slots gets 0.  The rows between are bf16: they
+ *   are off by 2^-8 of a value at most, the 8-bit rows by 1/254 of their largest anyway, and
+ *   fp32 rows would double the layer's traffic.
+ *   x: int8 [T][H] with x_scale fp32[T] (seedmm_add_norm writes them);  gate_up: E matrices
+ *   [2 I][H], gate rows 0 .. I - 1, up rows I .. 2 I - 1;  down: E matrices [H][I];
+ *   y: fp32 [T][H], overwritten: seedmm_add_norm's delta.
+ *   workspace: device scratch of seedmm_moe_i8_workspace_bytes(T, top_k, E, H, I) bytes, 16-byte
+ *   aligned; overlapping calls use different ones.
+ * Errors: those of the calls, before anything runs (but for SEEDMM_EHIP), SEEDMM_EINVAL also for H, I < 1, H
+ * or I above 131,071 and T*top_k above 2^30, SEEDMM_EWORKSPACE, SEEDMM_EALIGN (the workspace not 16-byte aligned).
+ */
+typedef struct seedmm_i8mat {
+    const int8_t *weight;   /* [E][M][K]                    */
+    const void *scales;     /* [E][M]                       */
+    int s_dtype;            /* SEEDMM_F32 or SEEDMM_BF16    */
+} seedmm_i8mat;
+
+size_t seedmm_moe_i8_workspace_bytes(int T, int top_k, int E, int H, int I);
+int seedmm_moe_i8(const int32_t *topk_ids, const float *topk_w, int T, int top_k, const int8_t *x,
+                  const float *x_scale, float *y, int E, int H, int I, seedmm_i8mat gate_up,
+                  seedmm_i8mat down, void *workspace, size_t workspace_bytes, void *hip_stream);
+
 /* Static description of a status code (the C engine's error convention: a plain C99
  * interface, NanoSeedLM README "How it works"). */
 const char *seedmm_strerror(int status);

@@ -14,8 +14,10 @@ CSRC = os.path.join(HERE, "csrc")
 SO = os.path.join(HERE, "libseedmm.so")
 BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = [os.path.join(CSRC, "seedmm.hip"), os.path.join(CSRC, "search.hip"),
-           os.path.join(CSRC, "expert_cache.hip"), os.path.join(CSRC, "dense.hip")]
+           os.path.join(CSRC, "expert_cache.hip"), os.path.join(CSRC, "dense.hip"),
+           os.path.join(CSRC, "i8_gemv.hip"), os.path.join(CSRC, "moe_rows.hip")]
 HEADERS = [os.path.join(CSRC, "seed_decode.hpp"), os.path.join(CSRC, "moe_layer.hpp"),
+           os.path.join(CSRC, "device_rows.hpp"),
            os.path.join(ROOT, "include", "seedmm.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -41,6 +41,10 @@ class SeedBlock(ctypes.Structure):
                                                "top_k", "E", "H", "I", "P")])
 
 
+class I8Mat(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("s_dtype", ctypes.c_int)]
+
+
 class SeedSide(ctypes.Structure):
     _fields_ = [("stream", ctypes.c_void_p), ("fork", ctypes.c_void_p),
                 ("join", ctypes.c_void_p)]
@@ -97,6 +101,16 @@ def _load():
     L.seedmm_moe_block_workspace_bytes.argtypes = [blk, i32]
     L.seedmm_moe_block.argtypes = [blk, p, i32, p, i32, p, p, p, i32, p, sz, p,
                                    ctypes.POINTER(SeedSide)]
+    L.seedmm_i8_gemv.argtypes = [p, p, i32, i32, p, p, i64, p, p, i32, i64, i32, i32, i32, p]
+    L.seedmm_moe_sort.argtypes = [p, i32, i32, i32, p, i32, i64, p, p, i64, p, i32, p, p, p, sz, p]
+    L.seedmm_moe_sort_workspace_bytes.restype = sz
+    L.seedmm_moe_sort_workspace_bytes.argtypes = [i32, i32, i32]
+    L.seedmm_moe_unsort.argtypes = [p, i32, i64, i32, p, p, p, i32, i64, i32, i32, i32, p]
+    L.seedmm_moe_unsort_grad.argtypes = [p, i32, i64, p, i32, i64, i32, p, p, p, i64, p, i32, i32, i32, p]
+    L.seedmm_swiglu.argtypes = [p, i32, i64, p, i32, i64, p, p, i32, i32, p]
+    L.seedmm_moe_i8_workspace_bytes.restype = sz
+    L.seedmm_moe_i8_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    L.seedmm_moe_i8.argtypes = [p, p, i32, i32, p, p, p, i32, i32, i32, I8Mat, I8Mat, p, sz, p]
     L.seedmm_strerror.restype = ctypes.c_char_p
     L.seedmm_strerror.argtypes = [i32]
     L.seedmm_version.restype = i32
@@ -106,7 +120,8 @@ def _load():
                  "seedmm_search_prepare", "seedmm_moe_mixed",
                  "seedmm_cache_init", "seedmm_cache_reset", "seedmm_cache_plan",
                  "seedmm_cache_moe", "seedmm_cache_stats", "seedmm_q4_gemv", "seedmm_add_norm",
-                 "seedmm_route", "seedmm_moe_block"):
+                 "seedmm_route", "seedmm_moe_block", "seedmm_i8_gemv", "seedmm_moe_sort",
+                 "seedmm_moe_unsort", "seedmm_moe_unsort_grad", "seedmm_swiglu", "seedmm_moe_i8"):
         getattr(L, name).restype = i32
     return L
 
@@ -122,7 +137,10 @@ EXPORTS = ("seedmm_gemv", "seedmm_gemv_ex", "seedmm_reconstruct", "seedmm_moe_di
            "seedmm_cache_init", "seedmm_cache_reset", "seedmm_cache_plan", "seedmm_cache_moe",
            "seedmm_cache_stats", "seedmm_q4_gemv", "seedmm_q4_workspace_bytes",
            "seedmm_add_norm", "seedmm_route",
-           "seedmm_moe_block_workspace_bytes", "seedmm_moe_block", "seedmm_strerror",
+           "seedmm_moe_block_workspace_bytes", "seedmm_moe_block", "seedmm_i8_gemv",
+           "seedmm_moe_sort", "seedmm_moe_sort_workspace_bytes", "seedmm_moe_unsort",
+           "seedmm_moe_unsort_grad", "seedmm_swiglu", "seedmm_moe_i8_workspace_bytes",
+           "seedmm_moe_i8", "seedmm_strerror",
            "seedmm_version")
 
 
@@ -625,6 +643,10 @@ def _load_binding():
     m.init(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value
              for n in ("seedmm_q4_gemv", "seedmm_q4_workspace_bytes", "seedmm_add_norm",
                        "seedmm_route")), SeedmmError)
+    m.init_experts(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value
+                     for n in ("seedmm_i8_gemv", "seedmm_moe_sort", "seedmm_moe_sort_workspace_bytes",
+                               "seedmm_moe_unsort", "seedmm_moe_unsort_grad", "seedmm_swiglu",
+                               "seedmm_moe_i8", "seedmm_moe_i8_workspace_bytes")))
     _dense = m
     return m
 
@@ -823,3 +845,136 @@ class MoeBlock:
                 ptr(w), T, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                 _current_stream_handle(dev) if handle is None else handle, sd), "seedmm_moe_block")
         return y
+
+
+# ---- routed experts in 8-bit integers ------------------------------------------------
+
+def i8_gemv(mat: dict, x: torch.Tensor, x_scale: torch.Tensor, M: int, K: int, y=None,
+            y_dtype=torch.float32, offsets=None, stream=None):
+    """y = x W^T in 8-bit integers with a scale a row and a channel (seedmm_i8_gemv).  mat:
+    {"weight": int8 [M*K], "scales": fp32 or bf16 [M]}; x int8 [N][K] (or [K]) with x_scale
+    fp32 [N]; y [N][M] (or [M]) fp32 or bf16.  offsets: int32 [E+1] of moe_sort, for rows sorted
+    by expert and E stacked matrices; rows of y behind offsets[E] are left as they were (a y
+    allocated here holds no values there)."""
+    if y is None:
+        if M < 0:
+            raise ValueError(f"M = {M} is out of range")
+        with _on(stream):
+            y = torch.empty((*_gpu(x, "x").shape[:-1], M), dtype=y_dtype, device=x.device)
+    (_dense or _load_binding()).i8_gemv(mat["weight"], mat["scales"], x, x_scale, y, offsets, M, K,
+                                        None if stream is None else _handle(stream, _gpu(x, "x")))
+    return y
+
+
+def moe_sort_workspace_bytes(T: int, top_k: int, E: int) -> int:
+    """Bytes of the workspace that moe_sort needs for T tokens."""
+    return int(_lib.seedmm_moe_sort_workspace_bytes(T, top_k, E))
+
+
+def moe_sort(x: torch.Tensor, topk_ids: torch.Tensor, E: int, x_scale=None, rows=None,
+             row_scale=None, offsets=None, inverse=None, workspace=None, stream=None):
+    """(rows, row_scale, offsets, inverse): the tokens' rows in the order of their experts
+    (seedmm_moe_sort).  x fp32, bf16 or int8 [T][H], with x_scale fp32 [T] or None; topk_ids
+    int32 [T][top_k], ids outside of [0, E) dropped.  rows [T*top_k][H] and row_scale (None
+    without x_scale) hold values up to row offsets[E]; offsets int32 [E+1]; inverse int32
+    [T][top_k], the row of each slot or -1."""
+    if rows is None or offsets is None or inverse is None or (x_scale is not None and row_scale is None):
+        if _gpu(topk_ids, "topk_ids").dim() != 2:
+            raise ValueError("topk_ids must be a contiguous [T][top_k] tensor")
+        n, dev = topk_ids.numel(), _gpu(x, "x").device
+        with _on(stream):
+            if rows is None:
+                rows = torch.empty((n, x.shape[-1]), dtype=x.dtype, device=dev)
+            if row_scale is None and x_scale is not None:
+                row_scale = torch.empty(n, dtype=torch.float32, device=dev)
+            if offsets is None:
+                offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+            if inverse is None:
+                inverse = torch.empty(topk_ids.shape, dtype=torch.int32, device=dev)
+    if stream is not None:
+        if workspace is None and _gpu(topk_ids, "topk_ids").dim() == 2:
+            need = moe_sort_workspace_bytes(*topk_ids.shape, E)
+            if need:       # scratch of a call on another stream belongs to that stream
+                with _on(stream):
+                    workspace = torch.empty(need, dtype=torch.uint8, device=_gpu(x, "x").device)
+        stream = _handle(stream, _gpu(x, "x"))
+    (_dense or _load_binding()).moe_sort(x, topk_ids, E, x_scale, rows, row_scale, offsets, inverse,
+                                         workspace, stream)
+    return rows, row_scale, offsets, inverse
+
+
+def moe_unsort(rows: torch.Tensor, inverse: torch.Tensor, topk_w=None, y=None,
+               y_dtype=torch.float32, stream=None):
+    """y [T][H] fp32 or bf16: each token's rows, weighted and summed (seedmm_moe_unsort).  rows
+    fp32 or bf16 [n][H]; inverse int32 [T][top_k] of moe_sort; topk_w fp32 [T][top_k] or None
+    (ones: the gradient of moe_sort's rows with respect to x)."""
+    if y is None:
+        with _on(stream):
+            y = torch.empty((_gpu(inverse, "inverse").shape[0], _gpu(rows, "rows").shape[-1]),
+                            dtype=y_dtype, device=rows.device)
+    (_dense or _load_binding()).moe_unsort(rows, inverse, topk_w, y,
+                                           None if stream is None else _handle(stream, _gpu(rows, "rows")))
+    return y
+
+
+def moe_unsort_grad(dy: torch.Tensor, rows: torch.Tensor, inverse: torch.Tensor,
+                    topk_w: torch.Tensor, drows=None, dw=None, stream=None):
+    """(drows, dw): moe_unsort's gradients for dy fp32 or bf16 [T][H] (seedmm_moe_unsort_grad).
+    drows has rows' shape and type (rows that no slot names are left as they were; a drows
+    allocated here holds no values there), dw is fp32 [T][top_k]."""
+    if drows is None or dw is None:
+        with _on(stream):
+            if drows is None:
+                drows = torch.empty(_gpu(rows, "rows").shape, dtype=rows.dtype, device=rows.device)
+            if dw is None:
+                dw = torch.empty(_gpu(inverse, "inverse").shape, dtype=torch.float32,
+                                 device=inverse.device)
+    (_dense or _load_binding()).moe_unsort_grad(
+        dy, rows, inverse, topk_w, drows, dw,
+        None if stream is None else _handle(stream, _gpu(rows, "rows")))
+    return drows, dw
+
+
+def swiglu(gate_up: torch.Tensor, out_dtype=torch.bfloat16, out=None, scale=None, count=None,
+           stream=None):
+    """(out, scale): silu(gate) * up of rows [N][2I] fp32 or bf16 that hold gate, then up
+    (seedmm_swiglu).  out [N][I] of out_dtype (float32, bfloat16, or int8 with scale fp32 [N];
+    scale is None otherwise).  count: int32 [1] on the GPU, the number of rows that exist
+    (offsets[E:] of moe_sort), or None for all."""
+    if out is None:
+        with _on(stream):
+            out = torch.empty((*_gpu(gate_up, "gate_up").shape[:-1], gate_up.shape[-1] // 2),
+                              dtype=out_dtype, device=gate_up.device)
+    if scale is None and out.dtype is torch.int8:
+        with _on(stream):
+            scale = torch.empty(_gpu(gate_up, "gate_up").shape[:-1] if gate_up.dim() > 1 else 1,
+                                dtype=torch.float32, device=gate_up.device)
+    (_dense or _load_binding()).swiglu(gate_up, out, scale, count,
+                                       None if stream is None else _handle(stream, _gpu(gate_up, "gate_up")))
+    return out, scale
+
+
+def moe_i8_workspace_bytes(T: int, top_k: int, E: int, H: int, I: int) -> int:
+    """Bytes of the workspace that moe_i8 needs for T tokens."""
+    return int(_lib.seedmm_moe_i8_workspace_bytes(T, top_k, E, H, I))
+
+
+def moe_i8(topk_ids, topk_w, x, x_scale, E, H, I, gate_up, down, y=None, workspace=None,
+           stream=None):
+    """y fp32 [T][H]: the routed SwiGLU layer of experts in 8-bit integers (seedmm_moe_i8).  x
+    int8 [T][H] with x_scale fp32 [T] (add_norm's); gate_up, down: matrices as for i8_gemv, E
+    stacked [2I][H] (gate rows, then up rows) and [H][I]; topk_ids int32 and topk_w fp32
+    [T][top_k], an id outside of [0, E) drops its slot."""
+    if y is None:
+        with _on(stream):
+            y = torch.empty(_gpu(x, "x").shape, dtype=torch.float32, device=x.device)
+    if stream is not None:
+        if workspace is None and _gpu(topk_ids, "topk_ids").dim() == 2:
+            with _on(stream):
+                workspace = torch.empty(moe_i8_workspace_bytes(*topk_ids.shape, E, H, I),
+                                        dtype=torch.uint8, device=_gpu(x, "x").device)
+        stream = _handle(stream, _gpu(x, "x"))
+    (_dense or _load_binding()).moe_i8(topk_ids, topk_w, x, x_scale, E, H, I, gate_up["weight"],
+                                       gate_up["scales"], down["weight"], down["scales"], y, workspace,
+                                       stream)
+    return y
