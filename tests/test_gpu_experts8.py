@@ -732,7 +732,10 @@ def test_two_calls_at_once(sm):
     streams = [torch.cuda.Stream() for _ in range(2)]
     for i, st in enumerate(streams):
         run, _ = everything(sm, T=600 + 300 * i, seed=40 + i, stream=st)
-        wants.append([o.clone() for o in run()])
+        torch.cuda.synchronize()
+        outs = run()
+        torch.cuda.synchronize()       # the calls are on st, the copies on the current stream
+        wants.append([o.clone() for o in outs])
         runs.append(run)
     torch.cuda.synchronize()
     for _ in range(5):
