@@ -21,13 +21,17 @@ __device__ __forceinline__ uint32_t wave_usum(uint32_t v) {
 // ----------------------------------------------------------------------------------
 // seedmm_moe_sort.  The place of pair p with expert e is
 //     #{pairs of experts below e} + #{pairs q < p of expert e},
-// a count over ids, so no pair waits for another and the order is always the same.  Batches
-// of up to kSortOnce pairs count over all ids in the workgroup that moves the token (one
-// launch).  Larger ones are cut into chunks: k_sort_count has each chunk's experts counted,
-// k_sort_scan sums the chunks in front, and k_sort counts inside the chunk only.
+// a count over ids, so no pair waits for another and the order is always the same.
+//   ONCE: batches of up to kSortOnce pairs count over all ids in the workgroup that moves the token:
+//     one launch.
+//   DIRECT: larger ones are cut into chunks, whose experts k_sort_count counts; each workgroup
+//     sums the chunks' counts itself and counts ids inside its own chunk only.
+//   SCANNED: where those sums are long, k_sort_scan and k_sort_base make them once for all.
 // ----------------------------------------------------------------------------------
-constexpr int kSortOnce = 2048;      // pairs
+constexpr int kSortOnce = 1024;      // pairs
 constexpr int kSortChunk = 1024;     // pairs of a chunk, rounded down to whole tokens
+constexpr int kSortDirect = 8192;    // counts that a workgroup sums itself
+enum { ONCE, DIRECT, SCANNED };
 
 struct SortArgs {
     const int32_t* ids;     // [T][k]
@@ -37,8 +41,8 @@ struct SortArgs {
     float* rs;
     int32_t* offsets;       // [E + 1]
     int32_t* inverse;       // [T][k]
-    int32_t* start;         // [chunks][E]: pairs of the expert in the chunks in front
-    int32_t* total;         // [E]
+    int32_t* count;         // [chunks][E] pairs of the expert in the chunk; scanned: in those in front
+    int32_t* total;         // [E] (scanned)
     int64_t ldx, ldr, row_bytes;
     int T, k, E, tokens, chunks;   // tokens of a chunk
 };
@@ -56,7 +60,7 @@ __global__ __launch_bounds__(256) void k_sort_count(const SortArgs a) {
         if (e < (uint32_t)a.E) atomicAdd(&hist[e], 1);   // whole numbers: any order, one sum
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += 256) a.start[c * a.E + e] = hist[e];
+    for (int e = threadIdx.x; e < a.E; e += 256) a.count[c * a.E + e] = hist[e];
 }
 
 // counts -> sums of the chunks in front, for 16 experts a workgroup; 16 threads an expert take
@@ -69,37 +73,24 @@ __global__ __launch_bounds__(256) void k_sort_scan(const SortArgs a) {
     const int64_t c1 = c0 + per < a.chunks ? c0 + per : a.chunks;
     int32_t sum = 0;
     if (e < a.E)
-        for (int64_t c = c0; c < c1; ++c) sum += a.start[c * a.E + e];
+        for (int64_t c = c0; c < c1; ++c) sum += a.count[c * a.E + e];
     part[run][col] = sum;
     __syncthreads();
     int32_t front = 0;
     for (int r = 0; r < run; ++r) front += part[r][col];
     if (e >= a.E) return;
     for (int64_t c = c0; c < c1; ++c) {
-        const int32_t v = a.start[c * a.E + e];
-        a.start[c * a.E + e] = front;
+        const int32_t v = a.count[c * a.E + e];
+        a.count[c * a.E + e] = front;
         front += v;
     }
     if (run == 15) a.total[e] = front;
 }
 
-// offsets[0 .. E] by one workgroup of 256 threads
-template <bool CHUNKED>
-__device__ void sort_offsets(const SortArgs& a, int32_t* hist) {
+// hist[0 .. E - 1] -> offsets[0 .. E], by one workgroup of 256 threads
+__device__ void write_offsets(const SortArgs& a, const int32_t* hist) {
     __shared__ int32_t wave_sums[4];
     const int tid = threadIdx.x;
-    if constexpr (CHUNKED) {
-        for (int e = tid; e < a.E; e += 256) hist[e] = a.total[e];
-    } else {
-        for (int e = tid; e < a.E; e += 256) hist[e] = 0;
-        __syncthreads();
-        const int n = a.T * a.k;
-        for (int i = tid; i < n; i += 256) {
-            const uint32_t e = (uint32_t)a.ids[i];
-            if (e < (uint32_t)a.E) atomicAdd(&hist[e], 1);
-        }
-    }
-    __syncthreads();
     const int per = (a.E + 255) / 256, e0 = tid * per;
     int32_t sum = 0;
     for (int i = 0; i < per; ++i) sum += e0 + i < a.E ? hist[e0 + i] : 0;
@@ -120,60 +111,103 @@ __device__ void sort_offsets(const SortArgs& a, int32_t* hist) {
     }
 }
 
-// Workgroup 0 of the first part writes the offsets; each other one places a token's pairs and
-// moves its row: the wave w counts for the slots w, w + 4, ... (a ballot counts 64 ids), then
-// all threads read the row once and write it to every place.
-template <bool CHUNKED>
+__global__ __launch_bounds__(256) void k_sort_base(const SortArgs a) { write_offsets(a, a.total); }
+
+// Workgroup 0 of the first part writes the offsets (k_sort_base has if SCANNED); each other one
+// places a token's pairs and moves its row: wave w counts for the slots w, w + 4, ... two at a time
+// (a ballot counts 64 ids), then all threads write the row, read at the start, to every place.
+// 4096 tokens of 8 slots and 2048 columns, 8 bits: 38.9 us with k_sort_count; a wave a token, four
+// to a workgroup, took 45.5, the writes then come from fewer tokens at once.
+template <int MODE>
 __global__ __launch_bounds__(256) void k_sort(const SortArgs a, int64_t first) {
-    extern __shared__ int32_t lds[];
+    extern __shared__ int32_t lds[];      // ids that count, then (DIRECT) the experts' sums
     __shared__ int32_t place[kMaxTopK];
     const int64_t b = first + blockIdx.x;
-    if (b == 0) return sort_offsets<CHUNKED>(a, lds);
-    const int64_t t = b - 1;
     const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t chunk = CHUNKED ? t / a.tokens : 0;
+    const int64_t t = b - 1;
+    const int64_t chunk = MODE != ONCE && b > 0 ? t / a.tokens : 0;
+    int32_t* total = lds + kSortChunk;    // DIRECT: pairs of an expert in all, and in the chunks in front
+    int32_t* front = total + a.E;
+    if constexpr (MODE == DIRECT) {
+        for (int e = tid; e < a.E; e += 256) {
+            int32_t all = 0, before = 0;
+#pragma unroll 8
+            for (int c = 0; c < a.chunks; ++c) {
+                const int32_t v = a.count[c * a.E + e];
+                all += v;
+                before += c < chunk ? v : 0;
+            }
+            total[e] = all;
+            front[e] = before;
+        }
+    }
+    if (b == 0) {
+        if constexpr (MODE == ONCE) {
+            for (int e = tid; e < a.E; e += 256) lds[e] = 0;
+            __syncthreads();
+            for (int i = tid; i < a.T * a.k; i += 256) {
+                const uint32_t e = (uint32_t)a.ids[i];
+                if (e < (uint32_t)a.E) atomicAdd(&lds[e], 1);
+            }
+        }
+        __syncthreads();
+        if constexpr (MODE != SCANNED) write_offsets(a, MODE == ONCE ? lds : total);
+        return;
+    }
+    const char* src = a.x + t * a.ldx;
+    const int64_t nv = a.row_bytes / 16;
+    // short rows: several slots at a time, `per` threads each
+    const int per = nv > 128 ? 256 : nv > 64 ? 128 : 64;
+    const int g = tid / per, groups = 256 / per, v0 = tid % per;
+    u32x4 w = {};
+    if (v0 < nv) __builtin_memcpy(&w, src + v0 * 16, 16);
     const int64_t q0 = chunk * a.tokens * a.k;
     const int p0 = (int)(t * a.k - q0);                          // the token's pairs in the chunk
-    const int n = CHUNKED ? p0 + a.k : a.T * a.k;                // pairs that count
+    const int n = MODE != ONCE ? p0 + a.k : a.T * a.k;           // pairs that count
     const int full = (n + 255) & ~255;                           // behind n: no expert
     for (int i = tid; i < full; i += 256) lds[i] = i < n ? a.ids[q0 + i] : -1;
     __syncthreads();
-    for (int s = wave; s < a.k; s += 4) {
-        const uint32_t e = (uint32_t)__builtin_amdgcn_readfirstlane(lds[p0 + s]);
-        int32_t at = -1;
-        if (e < (uint32_t)a.E) {
-            uint32_t count = 0;
-            if constexpr (CHUNKED) {
-                uint32_t below = 0;
-                for (int i = lane; i < (int)e; i += 64) below += (uint32_t)a.total[i];
-                count = wave_usum(below) + (uint32_t)a.start[chunk * a.E + e];
-            }
-            for (int i0 = 0; i0 < n; i0 += 256) {
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    for (int s = wave; s < a.k; s += 8) {
+        uint32_t e[2], count[2];
 #pragma unroll
-                for (int i = i0 + lane; i < i0 + 256; i += 64) {
-                    const uint32_t q = (uint32_t)lds[i];
-                    const bool in_front = (q == e && i < p0 + s) || (!CHUNKED && q < e);
-                    count += (uint32_t)__popcll(__ballot(in_front));
+        for (int j = 0; j < 2; ++j) {
+            const int sj = s + 4 * j < a.k ? s + 4 * j : s;
+            e[j] = (uint32_t)__builtin_amdgcn_readfirstlane(lds[p0 + sj]);
+            count[j] = 0;
+            if (MODE != ONCE && e[j] < (uint32_t)a.E) {
+                if constexpr (MODE == DIRECT) {
+                    uint32_t below = 0;
+                    for (int i = lane; i < (int)e[j]; i += 64) below += (uint32_t)total[i];
+                    count[j] = wave_usum(below) + (uint32_t)front[e[j]];
+                } else {
+                    count[j] = (uint32_t)a.offsets[e[j]] + (uint32_t)a.count[chunk * a.E + e[j]];
                 }
             }
-            at = (int32_t)count;
         }
-        if (lane == 0) {
-            place[s] = at;
-            a.inverse[t * a.k + s] = at;
+        for (int i0 = 0; i0 < n; i0 += 256) {
+#pragma unroll
+            for (int i = i0 + lane; i < i0 + 256; i += 64) {
+                const uint32_t q = (uint32_t)lds[i];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const bool in_front = (q == e[j] && i < p0 + s + 4 * j) || (MODE == ONCE && q < e[j]);
+                    count[j] += (uint32_t)__popcll(__ballot(in_front));
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (lane != 0 || s + 4 * j >= a.k) continue;
+            const int32_t at = e[j] < (uint32_t)a.E ? (int32_t)count[j] : -1;
+            place[s + 4 * j] = at;
+            a.inverse[t * a.k + s + 4 * j] = at;
             if (a.xs && at >= 0) a.rs[at] = a.xs[t];
         }
     }
     __syncthreads();
-    const char* src = a.x + t * a.ldx;
-    const int64_t nv = a.row_bytes / 16;
-    // Short rows: several slots at a time (`per` threads a slot)
-    const int per = nv >= 256 ? 256 : nv > 128 ? 256 : nv > 64 ? 128 : 64;
-    const int g = tid / per, groups = 256 / per;
-    for (int64_t v = tid % per; v < nv; v += per) {
-        u32x4 w;
-        __builtin_memcpy(&w, src + v * 16, 16);
+    for (int64_t v = v0; v < nv; v += per) {
+        if (v > v0) __builtin_memcpy(&w, src + v * 16, 16);
         for (int s = g; s < a.k; s += groups) {
             const int32_t at = place[s];
             if (at >= 0) __builtin_memcpy(a.rows + at * a.ldr + v * 16, &w, 16);
@@ -190,8 +224,10 @@ __global__ __launch_bounds__(256) void k_sort(const SortArgs a, int64_t first) {
 }
 
 // ----------------------------------------------------------------------------------
-// seedmm_moe_unsort and its gradients: TPR threads a token, 8 columns a thread and pass.  A
-// token's places and weights are uniform over a wave; the rows of 8 slots are in flight at once.
+// seedmm_moe_unsort and its gradients: TPR threads a token, 8 columns a thread and pass.  A lane a
+// slot loads the token's places and weights, and they are handed out by lane reads (loaded by every
+// lane for each slot and pass they cost 4096 tokens of 8 slots 39 us for 32.5); the rows of 8
+// slots are in flight at once.
 // ----------------------------------------------------------------------------------
 struct UnsortArgs {
     const void* rows;         // [n_rows][ldr]
@@ -201,42 +237,57 @@ struct UnsortArgs {
     const void* dy;           // [T][ldy] (gradients)
     void* drows;              // [n_rows][ldg] or null
     float* dw;                // [T][k] or null
-    int64_t ldr, ldy, ldg, t0, T;   // tokens from t0 on
+    int64_t ldr, ldy, ldg, tokens;
     uint32_t n_rows;
     int k, H, y_bf16;
 };
 
 constexpr int kSlots = 8;     // slots in flight
 
+// A token's places and weights, a slot a lane.
+struct Slots {
+    int32_t at = -1;
+    float w = 1.f;
+    __device__ __forceinline__ void load(const UnsortArgs& a, int64_t t) {
+        const int s = threadIdx.x & 63;
+        if (s < a.k) {
+            at = a.inverse[t * a.k + s];
+            if (a.w) w = a.w[t * a.k + s];
+        }
+    }
+    __device__ __forceinline__ uint32_t place(int s) const { return (uint32_t)__builtin_amdgcn_readlane(at, s); }
+    __device__ __forceinline__ float weight(int s) const { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), s)); }
+};
+
 template <int TPR, int RT>
 __global__ __launch_bounds__(256) void k_unsort(const UnsortArgs a) {
     const int tid = threadIdx.x;
-    const int64_t t = a.t0 + (int64_t)blockIdx.x * (256 / TPR) + __builtin_amdgcn_readfirstlane(tid / TPR);
-    if (t >= a.T) return;
-    const int32_t* inv = a.inverse + t * a.k;
-    const float* w = a.w ? a.w + t * a.k : nullptr;
-    for (int c = tid % TPR * 8; c < a.H; c += TPR * 8) {
-        const int n = a.H - c;
-        float sum[8] = {};
-        for (int s0 = 0; s0 < a.k; s0 += kSlots) {
-            Eight<RT> r[kSlots];
-            bool has[kSlots];
+    const int64_t hop = (int64_t)gridDim.x * (256 / TPR);
+    int64_t t = (int64_t)blockIdx.x * (256 / TPR) + __builtin_amdgcn_readfirstlane(tid / TPR);
+    for (; t < a.tokens; t += hop) {
+        Slots now;
+        now.load(a, t);
+        for (int c0 = 0; c0 < a.H; c0 += TPR * 8) {         // all lanes: they hold the places
+            const int c = c0 + tid % TPR * 8, n = a.H - c;
+            float sum[8] = {};
+            for (int s0 = 0; s0 < a.k; s0 += kSlots) {      // slots past k have no row
+                Eight<RT> r[kSlots];
 #pragma unroll
-            for (int s = 0; s < kSlots; ++s) {
-                const uint32_t at = s0 + s < a.k ? (uint32_t)inv[s0 + s] : 0xFFFFFFFFu;
-                has[s] = at < a.n_rows;
-                if (has[s]) r[s].load(a.rows, at * a.ldr + c, n);
+                for (int s = 0; s < kSlots; ++s) {
+                    const uint32_t at = now.place(s0 + s);
+                    if (at < a.n_rows) r[s].load(a.rows, at * a.ldr + c, n);
+                }
+#pragma unroll
+                for (int s = 0; s < kSlots; ++s) {
+                    if (now.place(s0 + s) >= a.n_rows) continue;
+                    const float f = now.weight(s0 + s);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[j] = __builtin_fmaf(f, r[s].get(j), sum[j]);
+                }
             }
-#pragma unroll
-            for (int s = 0; s < kSlots; ++s) {
-                if (!has[s]) continue;
-                const float f = w ? w[s0 + s] : 1.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) sum[j] = __builtin_fmaf(f, r[s].get(j), sum[j]);
-            }
+            if (a.y_bf16) store8<SEEDMM_BF16>(a.y, t * a.ldy + c, n, sum);
+            else store8<SEEDMM_F32>(a.y, t * a.ldy + c, n, sum);
         }
-        if (a.y_bf16) store8<SEEDMM_BF16>(a.y, t * a.ldy + c, n, sum);
-        else store8<SEEDMM_F32>(a.y, t * a.ldy + c, n, sum);
     }
 }
 
@@ -244,59 +295,59 @@ template <int TPR, int YT, int RT>
 __global__ __launch_bounds__(256) void k_unsort_grad(const UnsortArgs a) {
     __shared__ float red[4][kSlots];
     const int tid = threadIdx.x;
-    const int64_t t = a.t0 + (int64_t)blockIdx.x * (256 / TPR) + __builtin_amdgcn_readfirstlane(tid / TPR);
-    if (TPR < 256 && t >= a.T) return;          // no barrier below for these
-    const int32_t* inv = a.inverse + t * a.k;
-    for (int s0 = 0; s0 < a.k; s0 += kSlots) {
-        uint32_t at[kSlots];
-        float f[kSlots], dot[kSlots];
-#pragma unroll
-        for (int s = 0; s < kSlots; ++s) {
-            at[s] = s0 + s < a.k ? (uint32_t)inv[s0 + s] : 0xFFFFFFFFu;
-            f[s] = at[s] < a.n_rows ? a.w[t * a.k + s0 + s] : 0.f;
-            dot[s] = 0.f;
-        }
-        for (int c = tid % TPR * 8; c < a.H; c += TPR * 8) {
-            const int n = a.H - c;
-            Eight<YT> d;
-            Eight<RT> r[kSlots];
-            d.load(a.dy, t * a.ldy + c, n);
-            if (a.dw) {
-#pragma unroll
-                for (int s = 0; s < kSlots; ++s)
-                    if (at[s] < a.n_rows) r[s].load(a.rows, at[s] * a.ldr + c, n);
-            }
-#pragma unroll
-            for (int s = 0; s < kSlots; ++s) {
-                if (at[s] >= a.n_rows) continue;
+    const int64_t hop = (int64_t)gridDim.x * (256 / TPR);
+    int64_t t = (int64_t)blockIdx.x * (256 / TPR) + __builtin_amdgcn_readfirstlane(tid / TPR);
+    for (; t < a.tokens; t += hop) {
+        Slots now;
+        now.load(a, t);
+        for (int s0 = 0; s0 < a.k; s0 += kSlots) {
+            float dot[kSlots] = {};
+            for (int c0 = 0; c0 < a.H; c0 += TPR * 8) {     // all lanes: they hold the places
+                const int c = c0 + tid % TPR * 8, n = a.H - c;
+                Eight<YT> d;
+                Eight<RT> r[kSlots];
+                d.load(a.dy, t * a.ldy + c, n);
                 if (a.dw) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) dot[s] = __builtin_fmaf(d.get(j), r[s].get(j), dot[s]);
+                    for (int s = 0; s < kSlots; ++s) {
+                        const uint32_t at = now.place(s0 + s);
+                        if (at < a.n_rows) r[s].load(a.rows, at * a.ldr + c, n);
+                    }
                 }
-                if (a.drows) {
-                    float v[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = f[s] * d.get(j);
-                    store8<RT>(a.drows, at[s] * a.ldg + c, n, v);
+                for (int s = 0; s < kSlots; ++s) {
+                    const uint32_t at = now.place(s0 + s);
+                    if (at >= a.n_rows) continue;
+                    if (a.dw) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) dot[s] = __builtin_fmaf(d.get(j), r[s].get(j), dot[s]);
+                    }
+                    if (a.drows) {
+                        const float f = now.weight(s0 + s);
+                        float v[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] = f * d.get(j);
+                        store8<RT>(a.drows, at * a.ldg + c, n, v);
+                    }
                 }
             }
-        }
-        if (!a.dw) continue;
+            if (!a.dw) continue;
 #pragma unroll
-        for (int s = 0; s < kSlots; ++s) dot[s] = wave_sum(dot[s]);
-        if constexpr (TPR > 64) {
-            if (s0) __syncthreads();
-            if ((tid & 63) == 0) {
+            for (int s = 0; s < kSlots; ++s) dot[s] = wave_sum(dot[s]);
+            if constexpr (TPR > 64) {
+                __syncthreads();                       // the last sums have been read
+                if ((tid & 63) == 0) {
 #pragma unroll
-                for (int s = 0; s < kSlots; ++s) red[tid >> 6][s] = dot[s];
+                    for (int s = 0; s < kSlots; ++s) red[tid >> 6][s] = dot[s];
+                }
+                __syncthreads();
+                if (tid < kSlots && s0 + tid < a.k)
+                    a.dw[t * a.k + s0 + tid] = (red[0][tid] + red[1][tid]) + (red[2][tid] + red[3][tid]);
+            } else if ((tid & 63) == 0) {
+#pragma unroll
+                for (int s = 0; s < kSlots; ++s)
+                    if (s0 + s < a.k) a.dw[t * a.k + s0 + s] = dot[s];
             }
-            __syncthreads();
-            if (tid < kSlots && s0 + tid < a.k)
-                a.dw[t * a.k + s0 + tid] = (red[0][tid] + red[1][tid]) + (red[2][tid] + red[3][tid]);
-        } else if ((tid & 63) == 0) {
-#pragma unroll
-            for (int s = 0; s < kSlots; ++s)
-                if (s0 + s < a.k) a.dw[t * a.k + s0 + s] = dot[s];
         }
     }
 }
@@ -314,14 +365,18 @@ struct SwigluArgs {
     int I, out_dt;
 };
 
-// exp of -|g| cannot overflow: silu(g) = g / (1 + e) or, for g < 0, g e / (1 + e)
+// exp of -|g| cannot overflow: silu(g) = g / (1 + e) or, for g < 0, g e / (1 + e).  The reciprocal
+// of 1 .. 2 by the hardware's and a Newton step, half a step off like a division, in 4
+// instructions for its 10 (8-bit rows are bound by them).
 __device__ __forceinline__ float swiglu(float g, float u) {
-    const float e = expf(-fabsf(g));
-    return (g < 0.f ? g * e : g) / (1.f + e) * u;
+    const float e = expf(-fabsf(g)), d = 1.f + e;
+    float r = __builtin_amdgcn_rcpf(d);
+    r = __builtin_fmaf(__builtin_fmaf(-d, r, 1.f), r, r);
+    return (g < 0.f ? g * e : g) * r * u;
 }
 
-// the larger, a NaN above everything
-__device__ __forceinline__ float max_or_nan(float a, float b) { return a != a ? a : b != b ? b : fmaxf(a, b); }
+// |v| as a whole number: in the order of the values, a NaN above everything
+__device__ __forceinline__ uint32_t size_of(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
 // For 8 bits a row's scale and the scale's reciprocal (0: codes 0).
 struct CodeScale {
@@ -335,25 +390,27 @@ __device__ __forceinline__ CodeScale code_scale(float top) {
     return o;
 }
 
-template <int NW>     // waves that share a row
-__device__ __forceinline__ float row_top(float top, float* red) {
-    const uint32_t u = wave_umax(__float_as_uint(top));      // not negative: ordered as whole numbers, NaN on top
-    if constexpr (NW == 1) return __uint_as_float(u);
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = __uint_as_float(u);
-    __syncthreads();
-    float m = red[0];
+// the largest of a row's sizes; NW waves share a row
+template <int NW>
+__device__ __forceinline__ float row_top(uint32_t top, uint32_t* red) {
+    top = wave_umax(top);
+    if constexpr (NW > 1) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
+        __syncthreads();
 #pragma unroll
-    for (int i = 1; i < NW; ++i) m = max_or_nan(m, red[i]);
-    return m;
+        for (int i = 0; i < NW; ++i) top = top > red[i] ? top : red[i];
+    }
+    return __uint_as_float(top);
 }
 
 template <int TPR, int NP, int GT>
 __global__ __launch_bounds__(256) void k_swiglu(const SwigluArgs a) {
-    __shared__ float red[4];
+    __shared__ uint32_t red[4];
     const int tid = threadIdx.x;
     const int64_t n = a.n0 + (int64_t)blockIdx.x * (256 / TPR) + __builtin_amdgcn_readfirstlane(tid / TPR);
     if (n >= a.N || (a.count && n >= *a.count)) return;     // a whole workgroup where waves share a row
-    float h[NP][8], top = 0.f;
+    float h[NP][8];
+    uint32_t top = 0;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
         const int c = (p * TPR + tid % TPR) * 8, cnt = a.I - c;
@@ -364,7 +421,8 @@ __global__ __launch_bounds__(256) void k_swiglu(const SwigluArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             h[p][j] = swiglu(g.get(j), u.get(j));
-            top = max_or_nan(top, fabsf(h[p][j]));
+            const uint32_t v = j < cnt ? size_of(h[p][j]) : 0;
+            top = top > v ? top : v;
         }
     }
     float inv = 0.f;
@@ -392,7 +450,7 @@ __global__ __launch_bounds__(256) void k_swiglu(const SwigluArgs a) {
 // rows of any length, for 8 bits read twice
 template <int GT>
 __global__ __launch_bounds__(1024) void k_swiglu_long(const SwigluArgs a) {
-    __shared__ float red[16];
+    __shared__ uint32_t red[16];
     const int64_t n = a.n0 + blockIdx.x;
     if (a.count && n >= *a.count) return;
     auto piece = [&](int64_t c, float (&h)[8]) {
@@ -406,12 +464,12 @@ __global__ __launch_bounds__(1024) void k_swiglu_long(const SwigluArgs a) {
     };
     float inv = 0.f;
     if (a.out_dt == SEEDMM_I8) {
-        float top = 0.f;
+        uint32_t top = 0;
         for (int64_t c = threadIdx.x * 8; c < a.I; c += 8192) {
             float h[8];
             piece(c, h);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = max_or_nan(top, fabsf(h[j]));
+            for (int j = 0; j < 8; ++j) top = top > size_of(h[j]) ? top : size_of(h[j]);
         }
         const CodeScale o = code_scale(row_top<16>(top, red));
         if (threadIdx.x == 0) a.scale[n] = o.sc;
@@ -456,14 +514,17 @@ void launch_parts(K kernel, A a, int64_t A::* first, int64_t n, int threads, int
     }
 }
 
+// a grid that HIP takes (its workgroups go on to further tokens)
+unsigned bounded(int64_t groups) { return (unsigned)(groups < kLaunchThreads / 256 ? groups : kLaunchThreads / 256); }
+
 template <int TPR, int RT>
 void launch_unsort(const UnsortArgs& a, hipStream_t st) {
-    launch_parts(k_unsort<TPR, RT>, a, &UnsortArgs::t0, a.T, TPR, 256, st);
+    hipLaunchKernelGGL((k_unsort<TPR, RT>), dim3(bounded((a.tokens - 1) / (256 / TPR) + 1)), dim3(256), 0, st, a);
 }
 
 template <int TPR, int YT, int RT>
 void launch_grad(const UnsortArgs& a, hipStream_t st) {
-    launch_parts(k_unsort_grad<TPR, YT, RT>, a, &UnsortArgs::t0, a.T, TPR, 256, st);
+    hipLaunchKernelGGL((k_unsort_grad<TPR, YT, RT>), dim3(bounded((a.tokens - 1) / (256 / TPR) + 1)), dim3(256), 0, st, a);
 }
 
 template <int YT, int RT>
@@ -514,20 +575,24 @@ int seedmm_moe_sort(const int32_t* topk_ids, int T, int top_k, int E, const void
     SortArgs a = {topk_ids, (const char*)x, x_scale, (char*)rows, row_scale, offsets, inverse, nullptr, nullptr,
                   ldx * b, ldr * b, H * b, T, top_k, E, sort_tokens(top_k), (int)sort_chunks(T, top_k)};
     hipStream_t st = (hipStream_t)hip_stream;
-    const bool chunked = need != 0;
-    if (chunked) {
+    const int mode = need == 0 ? ONCE : (int64_t)a.chunks * E <= kSortDirect ? DIRECT : SCANNED;
+    if (mode != ONCE) {
         a.total = (int32_t*)workspace;
-        a.start = a.total + E;
+        a.count = a.total + E;
         hipLaunchKernelGGL(k_sort_count, dim3((unsigned)a.chunks), dim3(256), (size_t)E * 4, st, a);
-        hipLaunchKernelGGL(k_sort_scan, dim3((unsigned)((E + 15) / 16)), dim3(256), 0, st, a);
     }
-    const int held = chunked ? kSortChunk : (T * top_k + 255) & ~255;
-    const size_t lds = 4 * (size_t)(E > held ? E : held);
+    if (mode == SCANNED) {
+        hipLaunchKernelGGL(k_sort_scan, dim3((unsigned)((E + 15) / 16)), dim3(256), 0, st, a);
+        hipLaunchKernelGGL(k_sort_base, dim3(1), dim3(256), 0, st, a);
+    }
+    const int ids = (T * top_k + 255) & ~255;
+    const size_t lds = 4 * (size_t)(mode == ONCE ? (E > ids ? E : ids) : mode == DIRECT ? kSortChunk + 2 * E : kSortChunk);
     constexpr int64_t most = kLaunchThreads / 256;
     for (int64_t b0 = 0; b0 < (int64_t)T + 1; b0 += most) {     // the offsets, then a token a workgroup
-        const int64_t n = (int64_t)T + 1 - b0 < most ? (int64_t)T + 1 - b0 : most;
-        if (chunked) hipLaunchKernelGGL((k_sort<true>), dim3((unsigned)n), dim3(256), lds, st, a, b0);
-        else hipLaunchKernelGGL((k_sort<false>), dim3((unsigned)n), dim3(256), lds, st, a, b0);
+        const dim3 grid((unsigned)((int64_t)T + 1 - b0 < most ? (int64_t)T + 1 - b0 : most));
+        if (mode == ONCE) hipLaunchKernelGGL((k_sort<ONCE>), grid, dim3(256), lds, st, a, b0);
+        else if (mode == DIRECT) hipLaunchKernelGGL((k_sort<DIRECT>), grid, dim3(256), lds, st, a, b0);
+        else hipLaunchKernelGGL((k_sort<SCANNED>), grid, dim3(256), lds, st, a, b0);
     }
     return launch_status();
 }
@@ -540,7 +605,7 @@ int seedmm_moe_unsort(const void* rows, int r_dtype, int64_t ldr, int n_rows,
     if (T == 0 || H == 0) return SEEDMM_OK;
     if (!inverse || !y || (n_rows > 0 && !rows)) return SEEDMM_EINVAL;
     if (off_type(rows, r_dtype) || off_type(y, y_dtype) || off4(inverse) || off4(topk_w)) return SEEDMM_EALIGN;
-    UnsortArgs a = {rows, inverse, topk_w, y, nullptr, nullptr, nullptr, ldr, ldy, 0, 0, T, (uint32_t)n_rows,
+    UnsortArgs a = {rows, inverse, topk_w, y, nullptr, nullptr, nullptr, ldr, ldy, 0, T, (uint32_t)n_rows,
                     top_k, H, y_dtype == SEEDMM_BF16};
     hipStream_t st = (hipStream_t)hip_stream;
     const bool f = r_dtype == SEEDMM_F32;
@@ -561,7 +626,7 @@ int seedmm_moe_unsort_grad(const void* dy, int dy_dtype, int64_t ldd, const void
     if (off_type(dy, dy_dtype) || off_type(rows, r_dtype) || off_type(drows, r_dtype) || off4(inverse) ||
         off4(topk_w) || off4(dw))
         return SEEDMM_EALIGN;
-    UnsortArgs a = {rows, inverse, topk_w, nullptr, dy, drows, dw, ldr, ldd, ldg, 0, T, (uint32_t)n_rows, top_k, H, 0};
+    UnsortArgs a = {rows, inverse, topk_w, nullptr, dy, drows, dw, ldr, ldd, ldg, T, (uint32_t)n_rows, top_k, H, 0};
     hipStream_t st = (hipStream_t)hip_stream;
     const bool yf = dy_dtype == SEEDMM_F32, rf = r_dtype == SEEDMM_F32;
     if (yf) rf ? launch_grad<SEEDMM_F32, SEEDMM_F32>(a, st) : launch_grad<SEEDMM_F32, SEEDMM_BF16>(a, st);
