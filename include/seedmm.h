@@ -544,9 +544,9 @@ int seedmm_moe_block(const seedmm_block *block, void *r, int r_dtype, const void
  *   scale and then by the channel's, each rounded to fp32, and y rounded once: sum * x_scale
  *   has to be an fp32 number.  A scale of NaN gives a row or a column of NaN.
  * Errors: SEEDMM_EINVAL (null pointer, M, K or N < 0, M or N above 2^30, K above 131,071 (the
- * sums would leave int32), E outside [1, 4096], E != 1 without offsets, ldx < K, ldy < M, bad dtype),
- * SEEDMM_EALIGN (a pointer not aligned to its type), SEEDMM_EHIP.  M = 0 or N = 0 is an empty
- * success; with K = 0 the sums are 0 (weight and x may be NULL).
+ * sums would leave int32), E outside [1, 4096], E != 1 without offsets, ldx < K, ldy < M, bad
+ * dtype), SEEDMM_EALIGN (a pointer not aligned to its type), SEEDMM_EHIP.  M = 0 or N = 0 is an
+ * empty success; with K = 0 the sums are 0 (weight and x may be NULL).
  */
 int seedmm_i8_gemv(const int8_t *weight, const void *scales, int s_dtype, int E,
                    const int32_t *offsets, const int8_t *x, int64_t ldx, const float *x_scale,
@@ -569,9 +569,10 @@ int seedmm_i8_gemv(const int8_t *weight, const void *scales, int s_dtype, int E,
  *   workspace: device scratch of seedmm_moe_sort_workspace_bytes(T, top_k, E) bytes, 16-byte
  *   aligned, contents need not be initialised; NULL where that is 0 (small batches).  Calls
  *   that overlap in time use different ones.
- * Errors: SEEDMM_EINVAL (null pointer, T or H < 0, H above 2^30, top_k outside [1, 64], T*top_k >= 2^31, E
- * outside [1, 4096], ldx or ldr < H, bad dtype, one scale without the other), SEEDMM_EALIGN (a
- * pointer not aligned to its type), SEEDMM_EWORKSPACE, SEEDMM_EHIP.  T = 0 writes offsets of 0.
+ * Errors: SEEDMM_EINVAL (null pointer, T or H < 0, H above 2^30, top_k outside [1, 64], T*top_k
+ * >= 2^31, E outside [1, 4096], ldx or ldr < H, bad dtype, one scale without the other),
+ * SEEDMM_EALIGN (a pointer not aligned to its type, the workspace not 16-byte aligned),
+ * SEEDMM_EWORKSPACE, SEEDMM_EHIP.  T = 0 writes offsets of 0.
  */
 int seedmm_moe_sort(const int32_t *topk_ids, int T, int top_k, int E, const void *x, int x_dtype,
                     int64_t ldx, const float *x_scale, void *rows, int64_t ldr, float *row_scale,
@@ -597,8 +598,9 @@ size_t seedmm_moe_sort_workspace_bytes(int T, int top_k, int E);
  *   at most once.  drows may be rows itself with ldg = ldr; outputs overlap inputs in no other
  *   way.
  * Errors: SEEDMM_EINVAL (null pointer, T, H or n_rows < 0, H above 2^30, top_k outside [1, 64],
- * T*top_k >= 2^31, a leading dimension < H, bad dtype, rows as drows with another ld), SEEDMM_EALIGN (a pointer not aligned to its type), SEEDMM_EHIP.  T = 0 is an empty
- * success, and so is H = 0 but for dw, which is then 0.
+ * T*top_k >= 2^31, a leading dimension < H, bad dtype, rows as drows with another ld),
+ * SEEDMM_EALIGN (a pointer not aligned to its type), SEEDMM_EHIP.  T = 0 is an empty success,
+ * and so is H = 0 but for dw, which is then 0.
  */
 int seedmm_moe_unsort(const void *rows, int r_dtype, int64_t ldr, int n_rows,
                       const int32_t *inverse, const float *topk_w, void *y, int y_dtype,
@@ -640,8 +642,9 @@ int seedmm_swiglu(const void *gate_up, int g_dtype, int64_t ldg, void *out, int 
  *   y: fp32 [T][H], overwritten: seedmm_add_norm's delta.
  *   workspace: device scratch of seedmm_moe_i8_workspace_bytes(T, top_k, E, H, I) bytes, 16-byte
  *   aligned; overlapping calls use different ones.
- * Errors: those of the calls, before anything runs (but for SEEDMM_EHIP), SEEDMM_EINVAL also for H, I < 1, H
- * or I above 131,071 and T*top_k above 2^30, SEEDMM_EWORKSPACE, SEEDMM_EALIGN (the workspace not 16-byte aligned).
+ * Errors: those of the calls, before anything runs (but for SEEDMM_EHIP), SEEDMM_EINVAL also for
+ * H or I < 1 or above 131,071 and T*top_k above 2^30, SEEDMM_EWORKSPACE, SEEDMM_EALIGN (the
+ * workspace not 16-byte aligned).
  */
 typedef struct seedmm_i8mat {
     const int8_t *weight;   /* [E][M][K]                    */

@@ -30,6 +30,7 @@ __device__ __forceinline__ uint32_t wave_usum(uint32_t v) {
 // ----------------------------------------------------------------------------------
 constexpr int kSortOnce = 1024;      // pairs
 constexpr int kSortChunk = 1024;     // pairs of a chunk, rounded down to whole tokens
+static_assert(kSortOnce <= kSortChunk, "the ids of either fit the same shared memory");
 constexpr int kSortDirect = 8192;    // counts that a workgroup sums itself
 enum { ONCE, DIRECT, SCANNED };
 
@@ -585,8 +586,7 @@ int seedmm_moe_sort(const int32_t* topk_ids, int T, int top_k, int E, const void
         hipLaunchKernelGGL(k_sort_scan, dim3((unsigned)((E + 15) / 16)), dim3(256), 0, st, a);
         hipLaunchKernelGGL(k_sort_base, dim3(1), dim3(256), 0, st, a);
     }
-    const int ids = (T * top_k + 255) & ~255;
-    const size_t lds = 4 * (size_t)(mode == ONCE ? (E > ids ? E : ids) : mode == DIRECT ? kSortChunk + 2 * E : kSortChunk);
+    const size_t lds = 4 * (size_t)(mode == DIRECT ? kSortChunk + 2 * E : mode == ONCE && E > kSortOnce ? E : kSortChunk);
     constexpr int64_t most = kLaunchThreads / 256;
     for (int64_t b0 = 0; b0 < (int64_t)T + 1; b0 += most) {     // the offsets, then a token a workgroup
         const dim3 grid((unsigned)((int64_t)T + 1 - b0 < most ? (int64_t)T + 1 - b0 : most));
