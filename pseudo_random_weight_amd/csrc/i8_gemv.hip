@@ -96,6 +96,18 @@ __device__ __forceinline__ Rows find_rows(const I8Args& a, int64_t j, int tile) 
     return find_rows(a, j, tile, seek);
 }
 
+// The tiles of all experts.
+__device__ __forceinline__ int64_t count_tiles(const I8Args& a, int tile) {
+    int64_t all = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 64) {
+        const int e = e0 + (threadIdx.x & 63);
+        int n = 0;
+        if (e < a.E) n = clamp_row(a.offsets[e + 1], a.N) - clamp_row(a.offsets[e], a.N);
+        all += __builtin_amdgcn_readlane(wave_scan(n > 0 ? (n - 1) / tile + 1 : 0), 63);
+    }
+    return all;
+}
+
 #define INLINE __attribute__((always_inline))
 
 // A table of 16-byte pieces in LDS with C of them a row, read by 16 lanes at a time from 16
@@ -652,7 +664,16 @@ __global__ __launch_bounds__(256, 2) void k_i8_odd(const I8Args a) {
 // by hand.  One barrier a step is enough, and it stands in front of the step's last quarter, whose
 // operands are in registers: the matrix unit has work while the next step's first operands are read.
 //
-// Workgroups stay and take every 256th tile; the last steps of one already load the next.
+// Workgroups stay, one a CU; a tile's last steps already load the next.  Without experts a workgroup
+// takes every 256th tile.  With experts each XCD (every 8th workgroup) takes a stretch of the tiles,
+// an expert's in a row, so that its weights and rows come from memory to one L2 and every XCD has as
+// many tiles whatever the routing; and a tile of up to 128 rows, the rest of most experts, has half
+// of the products.  4096 tokens to 8 of 100 experts of 2048 x 2048: 214 us, 227 without both.
+//
+// 4096 x 8192 x 2048 (M x K, rows): 70 us, 8192 x 8192 x 8192: 435 us or 2530 TOP/s at 1.6 GHz, the clock
+// that the card's power leaves (1.9 GHz without the loads, 2.3 with a quarter of the products); 73%
+// of the cycles feed the matrix unit.  A tile's results take 7.8 us of 36 at K = 2048: all CUs write
+// at 4.3 TB/s then.  Not waiting for the stores in the next tile's first step gained nothing.
 // ----------------------------------------------------------------------------------
 constexpr int kWideStep = 128, kWideM = 256, kWideN = 256;
 
@@ -686,10 +707,17 @@ __device__ __forceinline__ WideBuffers wide_buffers(const I8Args& a, const WideT
 template <bool BF, bool SF32, bool REST>     // y in bf16, else fp32; scales in fp32, else bf16
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_i8_wide(const I8Args a, int64_t tiles) {
 #ifdef __HIP_DEVICE_COMPILE__      // buffer resources and LDS loads have no host form
-    constexpr int NB = 4, S = kWideStep, LW = kWideM / 32, L = LW + kWideN / 32, P = 4 * NB, O = 4 + NB;   // loads, products, operands
+    constexpr int S = kWideStep, LW = kWideM / 32, L = LW + kWideN / 32;   // loads
     __shared__ __align__(16) char w0[kWideM * S], w1[kWideM * S], x0[kWideN * S], x1[kWideN * S];
     __shared__ __align__(16) char pieces[2][4 * kPiece];
-    int64_t tile = blockIdx.x;
+    int64_t tile = blockIdx.x, hop = gridDim.x;
+    if (a.offsets) {
+        const int64_t all = count_tiles(a, kWideN) * a.tm;
+        const int xcd = blockIdx.x & 7;
+        hop = gridDim.x >> 3;
+        tile = all * xcd / 8 + (blockIdx.x >> 3);
+        tiles = all * (xcd + 1) / 8;
+    }
     Seek seek;
     WideTile cur = wide_tile(a, tile, tiles, seek);
     if (cur.r.n == 0) return;
@@ -703,11 +731,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     const int hopw = 32 * a.K, hopx = 32 * (int)a.ldx;
     // the lane's operands: piece 2 s + lane / 32 of row lane % 32 of each block of 32
     const int h = lane >> 5, fr = lane & 31;
-    const int wget = (wm * 128 + fr) * S, xget = (wn * 128 + fr) * S;
+    const int wget = (wm * 128 + fr) * S;
     const int real = ((a.K & ~15) + S - 1) / S, steps = (real + 1) & ~1;
 
-    i32x16 acc[4][NB];
-    i32x4 wf[2][4], xf[2][NB];
     // Of a tile's step t, piece n (0 .. L - 1) of this thread's.  Columns past K are zero in x: their
     // offset lies behind the buffer (the step's own stays inside of it).
     auto load = [&](const WideBuffers& d, int t, char* w, char* x, auto n) INLINE {
@@ -720,12 +746,6 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
             __builtin_amdgcn_raw_ptr_buffer_load_lds(d.x, (lds_ptr)(x + (i - LW) * 32 * S + wave * 1024), 16, (atx + (i - LW) * hopx) | past, k, 0, 0);
         }
     };
-    auto fetch = [&](const char* w, const char* x, int s, int to, auto n) INLINE {   // n: 0 .. 3 + NB
-        constexpr int i = n;
-        const int p = ((2 * s + h) ^ (fr >> 1 & 7)) * 16;
-        if constexpr (i < 4) wf[to][i] = *(const i32x4*)(w + wget + p + i * 32 * S);
-        else xf[to][i - 4] = *(const i32x4*)(x + xget + p + (i - 4) * 32 * S);
-    };
     // Every wave's loads of the next step have landed, and its reads of this step are done.
     auto arrive = [&]() INLINE { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
     constexpr std::integral_constant<int, 0> c0;
@@ -735,45 +755,44 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     each<L>([&](auto i) INLINE { load(now, 0, w0, x0, i); });
     each<L / 2>([&](auto i) INLINE { load(now, 1, w1, x1, i); });
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(L / 2) : "memory");
-    // A quarter of a step: its products, and in their shadow the next quarter's operands (read
-    // from w and x) over the first half of them and, for HALF 0 or 1, that half of the loads of
-    // d's step t to tw and tx over the second, in this order.
-    auto quarter = [&](const char* w, const char* x, int s, auto from, auto half, const WideBuffers& d, int t, char* tw, char* tx) INLINE {
-        each<P>([&](auto n) INLINE {
-            constexpr int p = n, F = from, HALF = half;
-            acc[p / NB][p % NB] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[F][p / NB], xf[F][p % NB], acc[p / NB][p % NB], 0, 0, 0);
-            each<O>([&](auto i) INLINE {
-                if constexpr (i * P / (2 * O) == p) fetch(w, x, s, F ^ 1, i);
-            });
-            if constexpr (HALF >= 0)
-                each<L / 2>([&](auto i) INLINE {
-                    if constexpr (P / 2 + i * P / L == p) load(d, t, tw, tx, std::integral_constant<int, HALF * (L / 2) + i>{});
+    // A tile of up to 64 NB rows, 32 NB of them a wave; `then`: the next tile's operands.
+    auto multiply = [&](auto nb, const WideBuffers& then) INLINE {
+        constexpr int NB = nb, P = 4 * NB, O = 4 + NB;     // products and operands of a quarter of a step
+        const int xget = (wn * 32 * NB + fr) * S;
+        i32x16 acc[4][NB];
+        i32x4 wf[2][4], xf[2][NB];
+        auto fetch = [&](const char* w, const char* x, int s, int to, auto n) INLINE {   // n: 0 .. 3 + NB
+            constexpr int i = n;
+            const int p = ((2 * s + h) ^ (fr >> 1 & 7)) * 16;
+            if constexpr (i < 4) wf[to][i] = *(const i32x4*)(w + wget + p + i * 32 * S);
+            else xf[to][i - 4] = *(const i32x4*)(x + xget + p + (i - 4) * 32 * S);
+        };
+        // A quarter of a step: its products, and in their shadow the next quarter's operands (read
+        // from w and x) over the first half of them and, for HALF 0 or 1, that half of the loads of
+        // d's step t to tw and tx over the second, in this order.
+        auto quarter = [&](const char* w, const char* x, int s, auto from, auto half, const WideBuffers& d, int t, char* tw, char* tx) INLINE {
+            each<P>([&](auto n) INLINE {
+                constexpr int p = n, F = from, HALF = half;
+                acc[p / NB][p % NB] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[F][p / NB], xf[F][p % NB], acc[p / NB][p % NB], 0, 0, 0);
+                each<O>([&](auto i) INLINE {
+                    if constexpr (i * P / (2 * O) == p) fetch(w, x, s, F ^ 1, i);
                 });
-            __builtin_amdgcn_sched_barrier(0);
-        });
-    };
-    // a step from (w, x); meanwhile the second half of d1's step t1 and the first of d2's t2
-    auto step = [&](char* w, char* x, char* nw, char* nx, const WideBuffers& d1, int t1, const WideBuffers& d2, int t2) INLINE {
-        asm volatile("" : "+v"(atw), "+v"(atx));     // their multiples are not kept
-        quarter(w, x, 1, c0, c1, d1, t1, nw, nx);
-        quarter(w, x, 2, c1, none, d1, 0, nw, nx);
-        quarter(w, x, 3, c0, none, d1, 0, nw, nx);
-        arrive();
-        quarter(nw, nx, 0, c1, c0, d2, t2, w, x);
-    };
-    for (;;) {
-        const WideTile next = wide_tile(a, tile + gridDim.x, tiles, seek);
-        const WideBuffers then = next.r.n ? wide_buffers(a, next) : now;
-        // the scales of the lane's channels and rows (0 where the tile has none)
-        f32x4 s[4][4];
-        float sx[NB];
-        const TileScales<SF32> sc(a, cur.r, cur.m0, cur.mrows);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) s[i][g] = sc.channels(wm * 128 + 4 * h + i * 32 + 8 * g);
-#pragma unroll
-        for (int j = 0; j < NB; ++j) sx[j] = sc.row(wn * 128 + j * 32 + fr);
+                if constexpr (HALF >= 0)
+                    each<L / 2>([&](auto i) INLINE {
+                        if constexpr (P / 2 + i * P / L == p) load(d, t, tw, tx, std::integral_constant<int, HALF * (L / 2) + i>{});
+                    });
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        };
+        // a step from (w, x); meanwhile the second half of d1's step t1 and the first of d2's t2
+        auto step = [&](char* w, char* x, char* nw, char* nx, const WideBuffers& d1, int t1, const WideBuffers& d2, int t2) INLINE {
+            asm volatile("" : "+v"(atw), "+v"(atx));     // their multiples are not kept
+            quarter(w, x, 1, c0, c1, d1, t1, nw, nx);
+            quarter(w, x, 2, c1, none, d1, 0, nw, nx);
+            quarter(w, x, 3, c0, none, d1, 0, nw, nx);
+            arrive();
+            quarter(nw, nx, 0, c1, c0, d2, t2, w, x);
+        };
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -786,13 +805,35 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
             step(w0, x0, w1, x1, now, t + 1, d, t2);
             step(w1, x1, w0, x0, d, t2, d, t2 + 1);
         }
+        // the sums stay where they are until each is read; the last product's end is waited for here
+        asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j) asm volatile("" : "+a"(acc[i][j]));
+        // the scales of the lane's channels and rows (0 where the tile has none)
+        f32x4 s[4][4];
+        float sx[NB];
+        const TileScales<SF32> sc(a, cur.r, cur.m0, cur.mrows);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) s[i][g] = sc.channels(wm * 128 + 4 * h + i * 32 + 8 * g);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) sx[j] = sc.row(wn * 32 * NB + j * 32 + fr);
         if constexpr (REST) multiply_rest(a, cur.r, cur.m0, cur.mrows, acc, wm, wn);
         write_sums<4, NB, BF>(a, cur.r, cur.m0, cur.mrows, acc, wm, wn, pieces[0] + wave * kPiece, pieces[1] + wave * kPiece,
                               [&](int i, int g) INLINE { return s[i][g]; }, [&](int j) INLINE { return sx[j]; });
+    };
+    for (;;) {
+        const WideTile next = wide_tile(a, tile += hop, tiles, seek);
+        const WideBuffers then = next.r.n ? wide_buffers(a, next) : now;
+        if (cur.r.n > 128) multiply(std::integral_constant<int, 4>{}, then);
+        else multiply(std::integral_constant<int, 2>{}, then);
         if (!next.r.n) break;
         cur = next;
         now = then;
-        tile += gridDim.x;
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");     // loads to LDS end before the workgroup does
 #endif
@@ -843,7 +884,7 @@ void launch_odd(const I8Args& a, hipStream_t st) {
 void launch_wide(I8Args a, hipStream_t st) {
     a.tm = (a.M - 1) / kWideM + 1;
     const int64_t tiles = row_tiles(a, kWideN) * a.tm;
-    const dim3 grid((unsigned)(tiles < 256 ? tiles : 256));
+    const dim3 grid((unsigned)(tiles < 256 && !a.offsets ? tiles : 256));
     by_types(a, [&](auto bf, auto sf) {
         if (a.K & 15) hipLaunchKernelGGL((k_i8_wide<bf, sf, true>), grid, dim3(256), 0, st, a, tiles);
         else hipLaunchKernelGGL((k_i8_wide<bf, sf, false>), grid, dim3(256), 0, st, a, tiles);
@@ -874,8 +915,9 @@ void launch_rows_jn(const I8Args& a, int jn, hipStream_t st) {
 //   Tiles of 128 channels by 64 or 128 rows: by 128 where that makes most of a workgroup a CU.
 //   256 x 8192 x 2048: 10.1 by 64, 11.7 by 128; 512 x 8192 x 2048: 17.1 and 14.1.
 //   Tiles of 256 by 256, one a CU: where there is one for nearly each CU.  1024 x 8192 x 2048: 33
-//   (128 by 128: 25.8), 2048 x 8192 x 2048: 42.6 (51.5); 100 experts of 2048 x 2048: 16384 rows 165
-//   (150), 32768 rows 224 (241).
+//   (128 by 128: 25.8), 2048 x 8192 x 2048: 42.6 (51.5).  With experts by their rows: 100 experts of
+//   2048 x 2048 with 164 rows each 152 (150), with 240 rows 176 (193), 328 rows 222 (244); 8 of
+//   8192 x 4096 with 128 rows 86 (80), with 192 rows 93 (104).
 void launch(I8Args a, hipStream_t st) {
     if (a.K < 16) {
         a.tm = (a.M - 1) / 64 + 1;
@@ -896,7 +938,7 @@ void launch(I8Args a, hipStream_t st) {
         int jn = avg <= (a.offsets ? 8 : 16) ? 1 : avg <= 32 ? 2 : 4;
         while (jn > 1 && row_tiles(a, 16 * jn) * ((a.M - 1) / 32 + 1) < 128) jn /= 2;
         odd ? launch_rows_jn<true>(a, jn, st) : launch_rows_jn<false>(a, jn, st);
-    } else if (!odd && (a.offsets ? avg >= 256 : row_tiles(a, 256) * ((a.M - 1) / 256 + 1) >= 224)) {
+    } else if (!odd && (a.offsets ? avg >= 176 : row_tiles(a, 256) * ((a.M - 1) / 256 + 1) >= 224)) {
         launch_wide(a, st);
     } else if (row_tiles(a, 128) * tm < 192) {
         odd ? launch_odd<2, 1>(a, st) : launch_mid<2, 1>(a, st);
