@@ -139,8 +139,8 @@ __device__ __forceinline__ u32x4 load16(const int8_t* row, int k, int K) {
     return v;
 }
 
-// A tile of 64 channels by 64 rows; each of four waves a quarter of it in 16 x 16 x 64
-// instructions, both operands through LDS.
+// Rows of fewer than 16 columns, which no 16-byte load fits: a tile of 64 channels by 64 rows, each of
+// four waves a quarter of it in 16 x 16 x 64 instructions, both operands through LDS.
 __global__ __launch_bounds__(256) void k_i8_tile(const I8Args a) {
     __shared__ u32x4 ws[64][5], xs[64][5];
     const int64_t b = a.first + blockIdx.x;
@@ -474,6 +474,10 @@ struct TileScales {
 // LDS holds rows of 64 bytes in 16-byte pieces, permuted (`piece`) so that 16 lanes reading a piece
 // of 16 rows meet 64 different banks.  Rows and columns that a tile does not have lie behind its
 // buffers and are zeros.
+//
+// 256 x 8192 x 2048 (rows, M, K): 10 us, 850 TOP/s; 100 experts of 2048 x 2048 with 41 rows each: 97 us,
+// 4.5 TB/s: bound by the weights there.  Tiles of 64 by 64 through registers took
+// 28 us for the first.
 // ----------------------------------------------------------------------------------
 constexpr int kStep = 64;              // bytes of K
 
@@ -577,7 +581,8 @@ __global__ __launch_bounds__(256, 2) void k_i8_mid(const I8Args a) {
 }
 
 // The same tiles for rows that do not start on 4 bytes: operands pass through registers, where the
-// words that hold a piece are shifted (Bytes16), to two buffers in LDS.
+// words that hold a piece are shifted (Bytes16), to two buffers in LDS.  256 x 8192 x 2049 (rows, M,
+// K): 25 us, 4096 rows 170; columns of 2052 take 10.5 and 81 by the kernels for 4 bytes.
 template <int MB, int NB, bool BF, bool SF32>
 __global__ __launch_bounds__(256, 2) void k_i8_odd(const I8Args a) {
 #ifdef __HIP_DEVICE_COMPILE__
