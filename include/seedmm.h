@@ -528,7 +528,8 @@ int seedmm_moe_block(const seedmm_block *block, void *r, int r_dtype, const void
  * the weighted sum of each token's rows, and seedmm_moe_i8 is the routed layer made of them.
  * Rows of any leading dimension and alignment (of their type) are taken; rows that start on 16
  * bytes are faster.  No result depends on the order in which anything runs: the same call
- * gives the same bits, and a token's result does not depend on the batch around it.
+ * gives the same bits, and a token's result does not depend on the batch around it.  Outputs
+ * overlap neither inputs nor each other, but where a call says so.
  *
  * seedmm_i8_gemv -- Y[n] = W X[n] for N rows of 8-bit integers with a scale a row, W in 8-bit
  * integers with a scale a channel, for one matrix or one an expert:

@@ -717,7 +717,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     __shared__ __align__(16) char pieces[2][4 * kPiece];
     int64_t tile = blockIdx.x, hop = gridDim.x;
     if (a.offsets) {
-        const int64_t all = count_tiles(a, kWideN) * a.tm;
+        int64_t all = count_tiles(a, kWideN) * a.tm;
+        all = all < tiles ? all : tiles;              // more only with wrong offsets
         const int xcd = blockIdx.x & 7;
         hop = gridDim.x >> 3;
         tile = all * xcd / 8 + (blockIdx.x >> 3);

@@ -58,10 +58,15 @@ __global__ __launch_bounds__(256) void k_sort_count(const SortArgs a) {
     __syncthreads();
     const int64_t p0 = c * a.tokens * a.k, all = (int64_t)a.T * a.k;
     const int n = (int)(all - p0 < a.tokens * a.k ? all - p0 : a.tokens * a.k);
-    for (int i = threadIdx.x; i < n; i += 256) {
-        const uint32_t e = (uint32_t)a.ids[p0 + i];
-        if (e < (uint32_t)a.E) atomicAdd(&hist[e], 1);   // whole numbers: any order, one sum
+    uint32_t e[kSortChunk / 256];
+#pragma unroll
+    for (int j = 0; j < kSortChunk / 256; ++j) {
+        const int i = threadIdx.x + 256 * j;
+        e[j] = i < n ? (uint32_t)a.ids[p0 + i] : ~0u;
     }
+#pragma unroll
+    for (int j = 0; j < kSortChunk / 256; ++j)
+        if (e[j] < (uint32_t)a.E) atomicAdd(&hist[e[j]], 1);   // whole numbers: any order, one sum
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += 256) a.count[c * a.E + e] = hist[e];
 }
