@@ -27,12 +27,11 @@ __device__ __forceinline__ uint32_t wave_usum(uint32_t v) {
 //   DIRECT: larger ones are cut into chunks, whose experts k_sort_count counts; each workgroup
 //     sums the chunks' counts itself and counts ids inside its own chunk only.
 //   SCANNED: where those sums are long, k_sort_scan and k_sort_base make them once for all.
-// Bound by the rows' copies: 4096 tokens of 8 slots over 100 experts, 2048 columns of 8 bits: 37 us,
-// 3.7 TB/s; 5 of them are k_sort_count and the launch between.  One token: 2.9 us, a launch.
+// Bound by the rows' copies: 4096 tokens of 8 slots over 100 experts, 2048 columns of 8 bits: 36 us,
+// 3.8 TB/s; 5 of them are k_sort_count and the launch between.  One token: 2.8 us, a launch.
 // ----------------------------------------------------------------------------------
 constexpr int kSortOnce = 1024;      // pairs
 constexpr int kSortChunk = 1024;     // pairs of a chunk, rounded down to whole tokens
-static_assert(kSortOnce <= kSortChunk, "the ids of either fit the same shared memory");
 constexpr int kSortDirect = 8192;    // counts that a workgroup sums itself
 enum { ONCE, DIRECT, SCANNED };
 
@@ -122,20 +121,23 @@ __device__ void write_offsets(const SortArgs& a, const int32_t* hist) {
 __global__ __launch_bounds__(256) void k_sort_base(const SortArgs a) { write_offsets(a, a.total); }
 
 // Workgroup 0 of the first part writes the offsets (k_sort_base has if SCANNED); each other one
-// places a token's pairs and moves its row: wave w counts for the slots w, w + 4, ... two at a time
-// (a ballot counts 64 ids), then all threads write the row, read at the start, to every place.
-// 4096 tokens of 8 slots and 2048 columns, 8 bits: 38.9 us with k_sort_count; a wave a token, four
-// to a workgroup, took 45.5, the writes then come from fewer tokens at once.
+// places a token's pairs and moves its row, read at the start.  ONCE: wave w counts for the slots w,
+// w + 4, ... two at a time (a ballot counts 64 ids).  Else a table in LDS gives each expert the
+// token's slot that names it, and each id in front of the token in its chunk adds one to its
+// expert's (with ballots 4096 tokens of 8 slots took 37.6 us for 36.1, 16384 of 16 slots 71 for 47).
+// A wave a token, four to a workgroup, took 45.5 us for 38.9: the writes then come from fewer
+// tokens at once.
 template <int MODE>
 __global__ __launch_bounds__(256) void k_sort(const SortArgs a, int64_t first) {
-    extern __shared__ int32_t lds[];      // ids that count, then (DIRECT) the experts' sums
-    __shared__ int32_t place[kMaxTopK];
+    extern __shared__ int32_t lds[];      // ONCE: all ids; else a slot of each expert, behind (DIRECT) the experts' sums
+    __shared__ int32_t place[kMaxTopK], named[kMaxTopK];
+    __shared__ uint32_t earlier[kMaxTopK];
     const int64_t b = first + blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 63;
     const int64_t t = b - 1;
     const int64_t chunk = MODE != ONCE && b > 0 ? t / a.tokens : 0;
-    int32_t* total = lds + kSortChunk;    // DIRECT: pairs of an expert in all, and in the chunks in front
-    int32_t* front = total + a.E;
+    int32_t* total = lds;                 // DIRECT: pairs of an expert in all, and in the chunks in front
+    int32_t* front = lds + a.E;
     if constexpr (MODE == DIRECT) {
         for (int e = tid; e < a.E; e += 256) {
             int32_t all = 0, before = 0;
@@ -171,49 +173,69 @@ __global__ __launch_bounds__(256) void k_sort(const SortArgs a, int64_t first) {
     if (v0 < nv) __builtin_memcpy(&w, src + v0 * 16, 16);
     const int64_t q0 = chunk * a.tokens * a.k;
     const int p0 = (int)(t * a.k - q0);                          // the token's pairs in the chunk
-    const int n = MODE != ONCE ? p0 + a.k : a.T * a.k;           // pairs that count
-    const int full = (n + 255) & ~255;                           // behind n: no expert
-    for (int i = tid; i < full; i += 256) lds[i] = i < n ? a.ids[q0 + i] : -1;
-    __syncthreads();
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    for (int s = wave; s < a.k; s += 8) {
-        uint32_t e[2], count[2];
+    if constexpr (MODE == ONCE) {
+        const int n = a.T * a.k, full = (n + 255) & ~255;        // behind n: no expert
+        for (int i = tid; i < full; i += 256) lds[i] = i < n ? a.ids[i] : -1;
+        __syncthreads();
+        for (int s = wave; s < a.k; s += 8) {
+            uint32_t e[2], count[2] = {0, 0};
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int sj = s + 4 * j < a.k ? s + 4 * j : s;
-            e[j] = (uint32_t)__builtin_amdgcn_readfirstlane(lds[p0 + sj]);
-            count[j] = 0;
-            if (MODE != ONCE && e[j] < (uint32_t)a.E) {
+            for (int j = 0; j < 2; ++j) e[j] = (uint32_t)__builtin_amdgcn_readfirstlane(lds[p0 + (s + 4 * j < a.k ? s + 4 * j : s)]);
+            for (int i0 = 0; i0 < n; i0 += 256) {
+#pragma unroll
+                for (int i = i0 + lane; i < i0 + 256; i += 64) {
+                    const uint32_t q = (uint32_t)lds[i];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        count[j] += (uint32_t)__popcll(__ballot((q == e[j] && i < p0 + s + 4 * j) || q < e[j]));
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (lane == 0 && s + 4 * j < a.k) place[s + 4 * j] = e[j] < (uint32_t)a.E ? (int32_t)count[j] : -1;
+        }
+    } else {
+        uint16_t* slot = (uint16_t*)(MODE == DIRECT ? lds + 2 * a.E : lds);
+        uint32_t id[kSortChunk / 256];
+#pragma unroll
+        for (int j = 0; j < kSortChunk / 256; ++j) id[j] = tid + 256 * j < p0 ? (uint32_t)a.ids[q0 + tid + 256 * j] : ~0u;
+        if (tid < a.k) {
+            const uint32_t e = (uint32_t)a.ids[t * a.k + tid];
+            named[tid] = (int32_t)e;
+            earlier[tid] = 0;
+            if (e < (uint32_t)a.E) slot[e] = (uint16_t)tid;      // one of its slots, if it has several
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kSortChunk / 256; ++j)
+            if (id[j] < (uint32_t)a.E) {
+                const uint32_t s = slot[id[j]];                  // any value where the token has no slot of the expert
+                if (s < (uint32_t)a.k && (uint32_t)named[s] == id[j]) atomicAdd(&earlier[s], 1);   // whole numbers
+            }
+        __syncthreads();
+        for (int s = wave; s < a.k; s += 4) {
+            const uint32_t e = (uint32_t)__builtin_amdgcn_readfirstlane(named[s]);
+            uint32_t at = ~0u;
+            if (e < (uint32_t)a.E) {
+                at = earlier[slot[e]] + (uint32_t)__popcll(__ballot(lane < s && (uint32_t)named[lane] == e));
                 if constexpr (MODE == DIRECT) {
                     uint32_t below = 0;
-                    for (int i = lane; i < (int)e[j]; i += 64) below += (uint32_t)total[i];
-                    count[j] = wave_usum(below) + (uint32_t)front[e[j]];
+                    for (int i = lane; i < (int)e; i += 64) below += (uint32_t)total[i];
+                    at += wave_usum(below) + (uint32_t)front[e];
                 } else {
-                    count[j] = (uint32_t)a.offsets[e[j]] + (uint32_t)a.count[chunk * a.E + e[j]];
+                    at += (uint32_t)a.offsets[e] + (uint32_t)a.count[chunk * a.E + e];
                 }
             }
-        }
-        for (int i0 = 0; i0 < n; i0 += 256) {
-#pragma unroll
-            for (int i = i0 + lane; i < i0 + 256; i += 64) {
-                const uint32_t q = (uint32_t)lds[i];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const bool in_front = (q == e[j] && i < p0 + s + 4 * j) || (MODE == ONCE && q < e[j]);
-                    count[j] += (uint32_t)__popcll(__ballot(in_front));
-                }
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (lane != 0 || s + 4 * j >= a.k) continue;
-            const int32_t at = e[j] < (uint32_t)a.E ? (int32_t)count[j] : -1;
-            place[s + 4 * j] = at;
-            a.inverse[t * a.k + s + 4 * j] = at;
-            if (a.xs && at >= 0) a.rs[at] = a.xs[t];
+            if (lane == 0) place[s] = (int32_t)at;
         }
     }
     __syncthreads();
+    if (tid < a.k) {
+        const int32_t at = place[tid];
+        a.inverse[t * a.k + tid] = at;
+        if (a.xs && at >= 0) a.rs[at] = a.xs[t];
+    }
     for (int64_t v = v0; v < nv; v += per) {
         if (v > v0) __builtin_memcpy(&w, src + v * 16, 16);
         for (int s = g; s < a.k; s += groups) {
@@ -597,7 +619,7 @@ int seedmm_moe_sort(const int32_t* topk_ids, int T, int top_k, int E, const void
         hipLaunchKernelGGL(k_sort_scan, dim3((unsigned)((E + 15) / 16)), dim3(256), 0, st, a);
         hipLaunchKernelGGL(k_sort_base, dim3(1), dim3(256), 0, st, a);
     }
-    const size_t lds = 4 * (size_t)(mode == DIRECT ? kSortChunk + 2 * E : mode == ONCE && E > kSortOnce ? E : kSortChunk);
+    const size_t lds = mode == ONCE ? 4 * (size_t)(E > kSortOnce ? E : kSortOnce) : (size_t)(E + 1) / 2 * 4 + (mode == DIRECT ? 8 * (size_t)E : 0);
     constexpr int64_t most = kLaunchThreads / 256;
     for (int64_t b0 = 0; b0 < (int64_t)T + 1; b0 += most) {     // the offsets, then a token a workgroup
         const dim3 grid((unsigned)((int64_t)T + 1 - b0 < most ? (int64_t)T + 1 - b0 : most));
