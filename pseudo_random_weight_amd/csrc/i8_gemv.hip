@@ -197,9 +197,13 @@ __global__ __launch_bounds__(256) void k_i8_tile(const I8Args a) {
 // 16 JN rows in 16 x 16 x 64 instructions, SB bytes of K a step; KW waves of a workgroup share a
 // channel tile and take its steps in turn, the next step's loads in flight while one is
 // multiplied.  Whole lines of the weights are loaded (SB / 16 lanes a row) and handed to the
-// lanes that multiply them through the wave's own piece of LDS; the activations, which the
-// caches hold, go straight to the lanes.  The sums are whole numbers: the waves' parts are added
-// in LDS in any order.
+// lanes that multiply them through the wave's own piece of LDS, and so are the activations of more
+// than 16 rows; those of up to 16, which the caches hold, go straight to the lanes.  The sums are
+// whole numbers: the waves' parts are added in LDS in any order.
+//
+// 131072 x 2048, 1 row: 45 us, 5.9 TB/s; 8 experts of 2048 x 2048: 8.2 us, 4.1 TB/s.  With more rows the load
+// path binds: 61 x 5125 x 4150 (rows, M, K) 12.9 us; pieces of 64 bytes straight to the lanes took 18.9
+// there and 29 for 64 x 8192 x 8192, which takes 22 now.
 //
 // Columns past K: as in the tiles of many rows, a piece that would pass the row's end is loaded
 // from its last 16 bytes in both operands, and the bytes of x in it that belong to earlier
@@ -208,24 +212,28 @@ __global__ __launch_bounds__(256) void k_i8_tile(const I8Args a) {
 constexpr int kRowsWaves = 8;
 
 // 16 bytes at any address.  Loads that do not start on 4 bytes take the memory path several times
-// as long (61 x 5125 x 4150: 28.9 us, 11.5 with rows of 4160), so where rows may start anywhere
+// as long (61 x 5125 x 4150: 28.9 us where rows of 4160 took 11.5), so where rows may start anywhere
 // (ODD) the aligned words that hold the 16 bytes are loaded and shifted; no other words are.
 template <bool ODD>
 struct Bytes16 {
     u32x4 v;
     uint32_t over, by;
-    __device__ __forceinline__ void load(const int8_t* p) {
+    // all: with the word behind the 16 bytes, if any of them lie in it
+    __device__ __forceinline__ void load(const int8_t* p, bool all = true) {
         if constexpr (ODD) {
             by = (uint32_t)(uintptr_t)p & 3;
             const int8_t* at = p - by;
             v = *(const u32x4*)__builtin_assume_aligned(at, 4);
-            over = *(const uint32_t*)(at + (by ? 16 : 12));
+            if (all) over = *(const uint32_t*)(at + (by ? 16 : 12));
         } else {
             __builtin_memcpy(&v, __builtin_assume_aligned(p, 4), 16);
         }
     }
-    __device__ __forceinline__ u32x4 get() const {
+    // all: as loaded; else the word is the next lane's first (every lane calls)
+    __device__ __forceinline__ u32x4 get(bool all = true) const {
         if constexpr (!ODD) return v;
+        const uint32_t next = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v[0], 0x101, 0xF, 0xF, true);
+        const uint32_t over = all ? this->over : next;
         u32x4 o;
         o[0] = __builtin_amdgcn_alignbyte(v[1], v[0], by);
         o[1] = __builtin_amdgcn_alignbyte(v[2], v[1], by);
@@ -239,7 +247,9 @@ template <int RM, int JN, int SB, int KW, bool ODD>
 __global__ __launch_bounds__(kRowsWaves * 64, JN > 1 ? 2 : 4) void k_i8_rows(const I8Args a) {
     constexpr int RW = kRowsWaves / KW, C = SB / 16, LR = 64 / C, LW = RM * 16 / LR, S = SB / 64;
     constexpr int CH = RW * RM * 16, TK = JN * 16;          // channels and rows of the workgroup
-    __shared__ u32x4 bounce[kRowsWaves][RM * 16 * C];
+    constexpr bool STAGED = JN > 1;                         // x through LDS, too
+    constexpr int LX = STAGED ? TK / LR : JN * S;
+    __shared__ u32x4 bounce[kRowsWaves][(RM * 16 + (STAGED ? TK : 0)) * C];
     __shared__ int32_t sums[TK][CH + 1];
     const int64_t tile = a.first + blockIdx.x;
     const Rows r = find_rows(a, tile / a.tm, TK);
@@ -249,7 +259,7 @@ __global__ __launch_bounds__(kRowsWaves * 64, JN > 1 ? 2 : 4) void k_i8_rows(con
     const int kw = wave % KW, rw = wave / KW;
     const int64_t mt = tile % a.tm * CH, m0 = mt + rw * RM * 16;
     for (int i = tid; i < TK * (CH + 1); i += kRowsWaves * 64) (&sums[0][0])[i] = 0;
-    // loads: piece lc of channels lr + LR i; operands: piece 4 s + q of channel or row c
+    // loads: piece lc of channels (and rows) lr + LR i; operands: piece 4 s + q of channel or row c
     const int lr = lane / C, lc = lane % C, c = lane & 15, q = lane >> 4;
     const int8_t* w[LW];
 #pragma unroll
@@ -257,39 +267,66 @@ __global__ __launch_bounds__(kRowsWaves * 64, JN > 1 ? 2 : 4) void k_i8_rows(con
         const int64_t m = m0 + lr + LR * i;
         w[i] = a.w + ((int64_t)r.e * a.M + (m < a.M ? m : a.M - 1)) * a.K;
     }
-    const int8_t* x[JN];
+    const int8_t* x[STAGED ? LX : JN];
 #pragma unroll
-    for (int j = 0; j < JN; ++j) x[j] = a.x + (r.row0 + (int64_t)min(j * 16 + c, r.n - 1)) * a.ldx;
-    Bytes16<ODD> wr[LW], xr[JN][S];
+    for (int j = 0; j < (STAGED ? LX : JN); ++j)
+        x[j] = a.x + (r.row0 + (int64_t)min(STAGED ? lr + LR * j : j * 16 + c, r.n - 1)) * a.ldx;
+    Bytes16<ODD> wr[LW], xr[LX];
+    // the word behind a piece is the next lane's first, but for a row's last pieces of the step or of K
+    auto own = [&](int k0) INLINE { return lc == C - 1 || k0 + 16 * lc + 32 > a.K; };
     auto load = [&](int k0) INLINE {
+        const bool more = own(k0);
 #pragma unroll
-        for (int i = 0; i < LW; ++i) wr[i].load(w[i] + min(k0 + 16 * lc, a.K - 16));
+        for (int i = 0; i < LW; ++i) wr[i].load(w[i] + min(k0 + 16 * lc, a.K - 16), more);
+        if constexpr (STAGED) {
 #pragma unroll
-        for (int s = 0; s < S; ++s)
+            for (int j = 0; j < LX; ++j) xr[j].load(x[j] + min(k0 + 16 * lc, a.K - 16), more);
+        } else {
 #pragma unroll
-            for (int j = 0; j < JN; ++j) xr[j][s].load(x[j] + min(k0 + 64 * s + 16 * q, a.K - 16));
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int j = 0; j < JN; ++j) xr[j * S + s].load(x[j] + min(k0 + 64 * s + 16 * q, a.K - 16), true);
+        }
+    };
+    // x's columns in front of column k that an earlier piece has, where a piece from K - 16 on stands for it
+    auto masked = [&](u32x4 v, int k) INLINE {
+        const int over = min(max(k - (a.K - 16), 0), 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] &= (uint32_t)(0xFFFFFFFFull << (8 * min(max(over - 4 * i, 0), 4)));
+        return v;
     };
     i32x4 acc[RM][JN] = {};
-    u32x4* mine = bounce[wave];
+    u32x4 *mine = bounce[wave], *rows = mine + RM * 16 * C;
     load(kw * SB);
     __syncthreads();
     for (int k0 = kw * SB; k0 < a.K; k0 += KW * SB) {
+        const bool last = k0 + SB > a.K, more = own(k0);
         wave_order();
 #pragma unroll
-        for (int i = 0; i < LW; ++i) mine[piece<C>(lr + LR * i, lc)] = wr[i].get();
+        for (int i = 0; i < LW; ++i) mine[piece<C>(lr + LR * i, lc)] = wr[i].get(more);
+        if constexpr (STAGED) {
+#pragma unroll
+            for (int j = 0; j < LX; ++j) {
+                u32x4 v = xr[j].get(more);
+                if (last) v = masked(v, k0 + 16 * lc);
+                rows[piece<C>(lr + LR * j, lc)] = v;
+            }
+        }
         wave_order();
         i32x4 xf[JN][S];
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            u32x4 keep = {~0u, ~0u, ~0u, ~0u};
-            if (k0 + SB > a.K) {
-                const int over = min(max(k0 + 64 * s + 16 * q - (a.K - 16), 0), 16);   // bytes of earlier pieces
+        for (int s = 0; s < S; ++s)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) keep[v] = (uint32_t)(0xFFFFFFFFull << (8 * min(max(over - 4 * v, 0), 4)));
+            for (int j = 0; j < JN; ++j) {
+                u32x4 v;
+                if constexpr (STAGED) {
+                    v = rows[piece<C>(j * 16 + c, 4 * s + q)];
+                } else {
+                    v = xr[j * S + s].get(true);
+                    if (last) v = masked(v, k0 + 64 * s + 16 * q);
+                }
+                xf[j][s] = __builtin_bit_cast(i32x4, v);
             }
-#pragma unroll
-            for (int j = 0; j < JN; ++j) xf[j][s] = __builtin_bit_cast(i32x4, xr[j][s].get() & keep);
-        }
         load(k0 + KW * SB);
 #pragma unroll
         for (int s = 0; s < S; ++s)
@@ -915,9 +952,11 @@ void launch_rows_jn(const I8Args& a, int jn, hipStream_t st) {
 // Which kernel (us, each on the other's side too; M x K, rows):
 //   fewer than 16 columns: k_i8_tile.
 //   Few rows (an expert has on average), or a grid of few tiles: k_i8_rows reads the weights once
-//   and splits K over a workgroup's waves.  8192 x 2048: 40 rows 8.6 (tiles of 64: 8.9), 49 rows
-//   9.3 (9.0), 256 rows 24.7 (10.1); 700 x 8190, 700 rows 30.6 (83); 100 experts of 2048 x 2048:
-//   512 rows 66 (71), 1024 rows 82.6 (80.7).
+//   and splits K over a workgroup's waves.  8192 x 2048: 49 rows 8.3 (tiles of 64: 9.2), 64 rows 8.2
+//   (9.3), 96 rows 11.0 (9.2); 4096 x 4096, 128 rows 10.7 (14.5); 16384 x 2048, 64 rows 11.7 (10.1);
+//   100 experts of 2048 x 2048 with 9 rows each 92.8 (86.2).  Rows on odd bytes: 8192 x 2049, 128
+//   rows 14.6 (23.9), 256 rows 26.2 (24.0); 1000 x 4097, 1024 rows 22 (46); 100 experts of 2048 x 2049
+//   with 16 rows each 126 (166), with 40 rows 174 (179), with 128 rows 330 (248).
 //   Tiles of 128 channels by 64 or 128 rows: by 128 where that makes most of a workgroup a CU.
 //   256 x 8192 x 2048: 10.1 by 64, 11.7 by 128; 512 x 8192 x 2048: 17.1 and 14.1.
 //   Tiles of 256 by 256, one a CU: where there is one for nearly each CU.  1024 x 8192 x 2048: 33
@@ -936,13 +975,16 @@ void launch(I8Args a, hipStream_t st) {
     const int avg = a.offsets ? (a.N - 1) / a.E + 1 : a.N;
     const int64_t tm = (a.M - 1) / 128 + 1, tiles64 = row_tiles(a, 64) * tm;
     // offsets inside a tile have to fit 31 bits
-    const bool tiled = a.ldx <= 1 << 22 && a.ldy <= 1 << 20 && avg >= (a.offsets ? 9 : 49) &&
-                       tiles64 >= (odd || a.K > 4096 ? 128 : 64);
+    const bool tiled = a.ldx <= 1 << 22 && a.ldy <= 1 << 20 && avg >= (a.offsets ? odd ? 33 : 9 : 49) &&
+                       tiles64 >= (odd ? 256 : 128);
     if (!tiled) {
-        // as many rows a wave as an expert has, but 128 channel tiles at least (us by 64, 32, 16 rows: 64 x
-        // 1000 x 4096 13.5 8.6 7.7; 300 x 500 x 5000 14.7 9.6 13.7; 61 x 5125 x 4150 18.4 20.9 29.6)
+        // as many rows a wave as an expert has, but enough waves' tiles (us by 64, 32, 16 rows: 61 x 5125 x 4150
+        // 13.0 15.4 29.7; 64 x 4096 x 4096 10.1 7.7; 300 x 500 x 5001 13.9 9.6 21; 64 x 1000 x 4096 9.7 6.8
+        // 7.8; 40 x 700 x 8192 13.7 9.7 8.6)
+        const int64_t tm32 = (a.M - 1) / 32 + 1;
         int jn = avg <= (a.offsets ? 8 : 16) ? 1 : avg <= 32 ? 2 : 4;
-        while (jn > 1 && row_tiles(a, 16 * jn) * ((a.M - 1) / 32 + 1) < 128) jn /= 2;
+        if (jn == 4 && row_tiles(a, 64) * tm32 < 144) jn = 2;
+        if (jn == 2 && row_tiles(a, 32) * tm32 < 64) jn = 1;
         odd ? launch_rows_jn<true>(a, jn, st) : launch_rows_jn<false>(a, jn, st);
     } else if (!odd && (a.offsets ? avg >= 176 : row_tiles(a, 256) * ((a.M - 1) / 256 + 1) >= 224)) {
         launch_wide(a, st);

@@ -31,7 +31,7 @@ def sm():
 # channels by 64 and by 128 rows; 256 by 256, one tile, several a workgroup, and tiles in the last
 # round for some of the workgroups only.  Columns 16 n, 16 n + 4 and odd for each.
 FEW = [(1, 33000, 80), (16, 9000, 2064), (3, 9000, 8208), (17, 70000, 144), (32, 20000, 1040), (30, 3000, 8224),
-       (33, 66000, 80), (48, 17000, 272), (64, 2000, 4112), (300, 200, 5008)]
+       (33, 66000, 80), (48, 17000, 272), (64, 2000, 4112), (300, 200, 5008), (61, 5125, 4144), (64, 4096, 2064)]
 MID = [(49, 8200, 2064), (100, 4100, 1040), (64, 4096, 4096), (256, 8190, 528), (257, 4097, 272), (1000, 1000, 4112),
        (512, 8200, 16), (513, 6400, 96)]
 WIDE = [(2000, 7200, 144), (2049, 8190, 272), (4100, 8190, 80), (3600, 4608, 16), (3585, 4100, 1040), (5000, 7000, 112)]
@@ -76,7 +76,7 @@ def test_tiles_of_each_type_on_4_bytes(sm, N, M, K, s, y, offset):
 GROUPED = [
     ([1] * 300, 0, 2000, 272), ([3, 0, 8, 5] * 30, 2, 700, 1040), ([9, 10] * 40, 0, 400, 528),
     ([40, 0, 70, 64, 65, 1] * 6, 0, 520, 272), ([200] * 12, 7, 1100, 144), ([0, 1000, 1, 255, 600, 0], 3, 520, 1040),
-    ([257] * 30, 0, 1030, 80), ([5000, 0, 0, 1], 0, 3000, 144), ([0] * 500 + [2100], 600, 4100, 48), ([0] * 64, 20000, 512, 64),
+    ([257] * 30, 0, 1030, 80), ([5000, 0, 0, 1], 0, 3000, 144), ([0] * 500 + [2100], 600, 4100, 48), ([0] * 64, 20000, 512, 64), ([16, 20, 11] * 20, 0, 300, 528),
 ]
 
 
