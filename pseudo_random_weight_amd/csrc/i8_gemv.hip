@@ -203,7 +203,7 @@ __global__ __launch_bounds__(256) void k_i8_tile(const I8Args a) {
 //
 // 131072 x 2048, 1 row: 45 us, 5.9 TB/s; 8 experts of 2048 x 2048: 8.2 us, 4.1 TB/s.  With more rows the load
 // path binds: 61 x 5125 x 4150 (rows, M, K) 12.9 us; pieces of 64 bytes straight to the lanes took 18.9
-// there and 29 for 64 x 8192 x 8192, which takes 22 now.
+// there and 28 for 64 x 8192 x 8192, which takes 21 now.
 //
 // Columns past K: as in the tiles of many rows, a piece that would pass the row's end is loaded
 // from its last 16 bytes in both operands, and the bytes of x in it that belong to earlier
@@ -272,7 +272,8 @@ __global__ __launch_bounds__(kRowsWaves * 64, JN > 1 ? 2 : 4) void k_i8_rows(con
     for (int j = 0; j < (STAGED ? LX : JN); ++j)
         x[j] = a.x + (r.row0 + (int64_t)min(STAGED ? lr + LR * j : j * 16 + c, r.n - 1)) * a.ldx;
     Bytes16<ODD> wr[LW], xr[LX];
-    // the word behind a piece is the next lane's first, but for a row's last pieces of the step or of K
+    // rows on any byte: the word behind a piece is the next lane's first, but for a row's last pieces of the
+    // step or of K (131072 x 2049, 1 row: 59 us, 64 with every word loaded)
     auto own = [&](int k0) INLINE { return lc == C - 1 || k0 + 16 * lc + 32 > a.K; };
     auto load = [&](int k0) INLINE {
         const bool more = own(k0);
@@ -285,15 +286,16 @@ __global__ __launch_bounds__(kRowsWaves * 64, JN > 1 ? 2 : 4) void k_i8_rows(con
 #pragma unroll
             for (int s = 0; s < S; ++s)
 #pragma unroll
-                for (int j = 0; j < JN; ++j) xr[j * S + s].load(x[j] + min(k0 + 64 * s + 16 * q, a.K - 16), true);
+                for (int j = 0; j < JN; ++j) xr[j * S + s].load(x[j] + min(k0 + 64 * s + 16 * q, a.K - 16));
         }
     };
     // x's columns in front of column k that an earlier piece has, where a piece from K - 16 on stands for it
-    auto masked = [&](u32x4 v, int k) INLINE {
+    auto kept = [&](int k) INLINE {
+        u32x4 keep = {~0u, ~0u, ~0u, ~0u};
         const int over = min(max(k - (a.K - 16), 0), 16);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] &= (uint32_t)(0xFFFFFFFFull << (8 * min(max(over - 4 * i, 0), 4)));
-        return v;
+        for (int i = 0; i < 4; ++i) keep[i] = (uint32_t)(0xFFFFFFFFull << (8 * min(max(over - 4 * i, 0), 4)));
+        return keep;
     };
     i32x4 acc[RM][JN] = {};
     u32x4 *mine = bounce[wave], *rows = mine + RM * 16 * C;
@@ -305,28 +307,23 @@ __global__ __launch_bounds__(kRowsWaves * 64, JN > 1 ? 2 : 4) void k_i8_rows(con
 #pragma unroll
         for (int i = 0; i < LW; ++i) mine[piece<C>(lr + LR * i, lc)] = wr[i].get(more);
         if constexpr (STAGED) {
+            u32x4 keep = {~0u, ~0u, ~0u, ~0u};
+            if (last) keep = kept(k0 + 16 * lc);
 #pragma unroll
-            for (int j = 0; j < LX; ++j) {
-                u32x4 v = xr[j].get(more);
-                if (last) v = masked(v, k0 + 16 * lc);
-                rows[piece<C>(lr + LR * j, lc)] = v;
-            }
+            for (int j = 0; j < LX; ++j) rows[piece<C>(lr + LR * j, lc)] = xr[j].get(more) & keep;
         }
         wave_order();
         i32x4 xf[JN][S];
 #pragma unroll
-        for (int s = 0; s < S; ++s)
+        for (int s = 0; s < S; ++s) {
+            u32x4 keep = {~0u, ~0u, ~0u, ~0u};
+            if (!STAGED && last) keep = kept(k0 + 64 * s + 16 * q);
 #pragma unroll
             for (int j = 0; j < JN; ++j) {
-                u32x4 v;
-                if constexpr (STAGED) {
-                    v = rows[piece<C>(j * 16 + c, 4 * s + q)];
-                } else {
-                    v = xr[j * S + s].get(true);
-                    if (last) v = masked(v, k0 + 64 * s + 16 * q);
-                }
-                xf[j][s] = __builtin_bit_cast(i32x4, v);
+                if constexpr (STAGED) xf[j][s] = __builtin_bit_cast(i32x4, rows[piece<C>(j * 16 + c, 4 * s + q)]);
+                else xf[j][s] = __builtin_bit_cast(i32x4, xr[j * S + s].get() & keep);
             }
+        }
         load(k0 + KW * SB);
 #pragma unroll
         for (int s = 0; s < S; ++s)
