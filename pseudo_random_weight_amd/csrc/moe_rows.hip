@@ -386,9 +386,9 @@ __global__ __launch_bounds__(256) void k_unsort_grad(const UnsortArgs a) {
 
 // ----------------------------------------------------------------------------------
 // seedmm_swiglu.  TPR threads a row, NP pieces of 8 columns a thread held in registers; for 8
-// bits the row's largest |h| is found before the codes are written.  Bound by memory: 29491 of 32768
-// rows of 1024, bf16, in 38 us (4.8 TB/s), to 8 bits in 47 (3.2; the arithmetic counts there: 55 with
-// divisions); 512 rows to 8 bits 3.2 us.
+// bits the row's largest |h| is found before the codes are written.  To floats bound by memory: 29491
+// of 32768 rows of 1024, bf16 to bf16, in 37 us (4.9 TB/s; 41 with a division).  To 8 bits by the arithmetic:
+// 43 us (3.5 TB/s; 55 with divisions).  512 rows to 8 bits 3.4 us, a launch.
 // ----------------------------------------------------------------------------------
 struct SwigluArgs {
     const void* gu;           // [N][ldg]
@@ -399,14 +399,19 @@ struct SwigluArgs {
     int I, out_dt;
 };
 
-// exp of -|g| cannot overflow: silu(g) = g / (1 + e) or, for g < 0, g e / (1 + e).  The reciprocal
-// of 1 .. 2 by the hardware's and a Newton step, half a step off like a division, in 4
-// instructions for its 10 (8-bit rows are bound by them).
+// exp of -|g| cannot overflow: silu(g) = n / d with d = 1 + e of 1 .. 2 and n = g or, for g < 0, g e.
+// The hardware's reciprocal r is a step off: 1 - d r is exact, and n r + n r (1 - d r) rounds once, 2^-22
+// of a step off a division, in 6 instructions for its 10.  (Where n is an infinity, d is 1 and the
+// second term NaN; the median of it and the largest numbers is one of these, and the sum n.)
+// 8-bit codes, which are bound by the arithmetic, take a corrected reciprocal times n, in 4: half a step of
+// fp32 more, 2^-17 of a code's step.
+template <bool CODES>
 __device__ __forceinline__ float swiglu(float g, float u) {
-    const float e = expf(-fabsf(g)), d = 1.f + e;
-    float r = __builtin_amdgcn_rcpf(d);
-    r = __builtin_fmaf(__builtin_fmaf(-d, r, 1.f), r, r);
-    return (g < 0.f ? g * e : g) * r * u;
+    const float e = expf(-fabsf(g)), d = 1.f + e, n = g < 0.f ? g * e : g;
+    const float r = __builtin_amdgcn_rcpf(d), off = __builtin_fmaf(-d, r, 1.f);
+    if constexpr (CODES) return n * __builtin_fmaf(off, r, r) * u;
+    const float more = __builtin_amdgcn_fmed3f(n * (off * r), -__FLT_MAX__, __FLT_MAX__);
+    return __builtin_fmaf(n, r, more) * u;
 }
 
 // |v| as a whole number: in the order of the values, a NaN above everything
@@ -437,7 +442,7 @@ __device__ __forceinline__ float row_top(uint32_t top, uint32_t* red) {
     return __uint_as_float(top);
 }
 
-template <int TPR, int NP, int GT>
+template <int TPR, int NP, int GT, bool CODES>
 __global__ __launch_bounds__(256) void k_swiglu(const SwigluArgs a) {
     __shared__ uint32_t red[4];
     const int tid = threadIdx.x;
@@ -454,13 +459,13 @@ __global__ __launch_bounds__(256) void k_swiglu(const SwigluArgs a) {
         u.load(a.gu, n * a.ldg + a.I + c, cnt);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            h[p][j] = swiglu(g.get(j), u.get(j));
+            h[p][j] = swiglu<CODES>(g.get(j), u.get(j));
             const uint32_t v = j < cnt ? size_of(h[p][j]) : 0;
             top = top > v ? top : v;
         }
     }
     float inv = 0.f;
-    if (a.out_dt == SEEDMM_I8) {
+    if constexpr (CODES) {
         const CodeScale o = code_scale(row_top<TPR / 64>(top, red));
         if (tid % TPR == 0) a.scale[n] = o.sc;
         inv = o.inv;
@@ -469,7 +474,7 @@ __global__ __launch_bounds__(256) void k_swiglu(const SwigluArgs a) {
     for (int p = 0; p < NP; ++p) {
         const int c = (p * TPR + tid % TPR) * 8, cnt = a.I - c;
         if (cnt <= 0) continue;
-        if (a.out_dt == SEEDMM_I8) {
+        if constexpr (CODES) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) h[p][j] = code_of(h[p][j], inv);
             store8<SEEDMM_I8>(a.out, n * a.ldo + c, cnt, h[p]);
@@ -482,7 +487,7 @@ __global__ __launch_bounds__(256) void k_swiglu(const SwigluArgs a) {
 }
 
 // rows of any length, for 8 bits read twice
-template <int GT>
+template <int GT, bool CODES>
 __global__ __launch_bounds__(1024) void k_swiglu_long(const SwigluArgs a) {
     __shared__ uint32_t red[16];
     const int64_t n = a.n0 + blockIdx.x;
@@ -493,11 +498,11 @@ __global__ __launch_bounds__(1024) void k_swiglu_long(const SwigluArgs a) {
         g.load(a.gu, n * a.ldg + c, cnt);
         u.load(a.gu, n * a.ldg + a.I + c, cnt);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = swiglu(g.get(j), u.get(j));
+        for (int j = 0; j < 8; ++j) h[j] = swiglu<CODES>(g.get(j), u.get(j));
         return cnt;
     };
     float inv = 0.f;
-    if (a.out_dt == SEEDMM_I8) {
+    if constexpr (CODES) {
         uint32_t top = 0;
         for (int64_t c = threadIdx.x * 8; c < a.I; c += 8192) {
             float h[8];
@@ -512,7 +517,7 @@ __global__ __launch_bounds__(1024) void k_swiglu_long(const SwigluArgs a) {
     for (int64_t c = threadIdx.x * 8; c < a.I; c += 8192) {
         float h[8];
         const int cnt = piece(c, h);
-        if (a.out_dt == SEEDMM_I8) {
+        if constexpr (CODES) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) h[j] = code_of(h[j], inv);
             store8<SEEDMM_I8>(a.out, n * a.ldo + c, cnt, h);
@@ -567,18 +572,23 @@ void launch_grad(const UnsortArgs& a, hipStream_t st) {
     else launch_grad<256, YT, RT>(a, st);
 }
 
-template <int TPR, int NP, int GT>
+template <int TPR, int NP, int GT, bool CODES>
 void launch_swiglu(const SwigluArgs& a, hipStream_t st) {
-    launch_parts(k_swiglu<TPR, NP, GT>, a, &SwigluArgs::n0, a.N, TPR, 256, st);
+    launch_parts(k_swiglu<TPR, NP, GT, CODES>, a, &SwigluArgs::n0, a.N, TPR, 256, st);
 }
 
-template <int GT>
+template <int GT, bool CODES>
 void launch_swiglu(const SwigluArgs& a, hipStream_t st) {
-    if (a.I <= 512) launch_swiglu<64, 1, GT>(a, st);
-    else if (a.I <= 2048) launch_swiglu<256, 1, GT>(a, st);
-    else if (a.I <= 4096) launch_swiglu<256, 2, GT>(a, st);
-    else if (a.I <= 8192) launch_swiglu<256, 4, GT>(a, st);
-    else launch_parts(k_swiglu_long<GT>, a, &SwigluArgs::n0, a.N, 1024, 1024, st);
+    if (a.I <= 512) launch_swiglu<64, 1, GT, CODES>(a, st);
+    else if (a.I <= 2048) launch_swiglu<256, 1, GT, CODES>(a, st);
+    else if (a.I <= 4096) launch_swiglu<256, 2, GT, CODES>(a, st);
+    else if (a.I <= 8192) launch_swiglu<256, 4, GT, CODES>(a, st);
+    else launch_parts(k_swiglu_long<GT, CODES>, a, &SwigluArgs::n0, a.N, 1024, 1024, st);
+}
+
+template <bool CODES>
+void launch_swiglu(const SwigluArgs& a, bool f32, hipStream_t st) {
+    f32 ? launch_swiglu<SEEDMM_F32, CODES>(a, st) : launch_swiglu<SEEDMM_BF16, CODES>(a, st);
 }
 
 }  // namespace
@@ -676,7 +686,8 @@ int seedmm_swiglu(const void* gate_up, int g_dtype, int64_t ldg, void* out, int 
     if (off_type(gate_up, g_dtype) || off_type(out, out_dtype) || off4(scale) || off4(count)) return SEEDMM_EALIGN;
     const SwigluArgs a = {gate_up, out, scale, count, ldg, ldo, 0, N, I, out_dtype};
     hipStream_t st = (hipStream_t)hip_stream;
-    g_dtype == SEEDMM_F32 ? launch_swiglu<SEEDMM_F32>(a, st) : launch_swiglu<SEEDMM_BF16>(a, st);
+    const bool f32 = g_dtype == SEEDMM_F32;
+    out_dtype == SEEDMM_I8 ? launch_swiglu<true>(a, f32, st) : launch_swiglu<false>(a, f32, st);
     return launch_status();
 }
 

@@ -1,0 +1,40 @@
+"""GPU tests of the operators of 8-bit experts at the borders of what their documentation
+promises: rounding, what is read and written, many experts, and replays with other routings."""
+import sys
+
+import pytest
+
+from test_gpu_experts8 import gen, swiglu64
+
+pytestmark = pytest.mark.gpu
+
+
+def say(*a):
+    print("[case]", *a, file=sys.stderr, flush=True)
+
+
+@pytest.fixture(scope="module")
+def sm():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a HIP device"
+    from pseudo_random_weight_amd import seedmm
+    return seedmm
+
+
+# ---- SwiGLU's rounding -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("I", [256, 1024, 4000, 8000, 16384])
+def test_swiglu_rounds_its_quotient_once(sm, I):
+    """Gates of 4 .. 8 times a power of two: half a step of fp32 for the sum 1 + e, half a step for the
+    quotient, and exp's step (2 half steps at most) times e / (1 + e) <= e^-4 = 0.0184: 2.04 half
+    steps.  A quotient made of a reciprocal and a product has one rounding more."""
+    import torch
+    say("swiglu rounding", I)
+    g = gen(I)
+    N = (1 << 20) // I
+    gu = torch.empty(N, 2 * I, device="cuda")
+    gu[:, :I] = 4 + 4 * torch.rand(N, I, generator=g, device="cuda")
+    gu[:, I:] = torch.tensor([1.0, -0.5, 4.0, 2.0 ** -20], device="cuda")[torch.randint(0, 4, (N, I), generator=g, device="cuda")]
+    got, want = sm.swiglu(gu, out_dtype=torch.float32)[0].double(), swiglu64(gu)
+    off = float(((got - want) / want).abs().max()) * 2.0 ** 24
+    assert off <= 2.04, off
