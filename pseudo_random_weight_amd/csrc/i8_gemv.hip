@@ -433,14 +433,23 @@ __device__ __forceinline__ void write_sums(const I8Args& a, const Rows& r, int64
                 if (BF && it >= 2) o = u32x4{o[2], o[3], o[0], o[1]};
                 __builtin_amdgcn_raw_buffer_store_b128(o, ybuf, yat + (j * 32 + it * 8) * (int)a.ldy * B + k * 128, 0, 0);
             }
-        } else {                                  // the last channels: one at a time
+        } else {                                  // the last channels: a row's last piece one at a time
+            const int left = mleft - k * CH - c * (16 / B);      // of this lane's
 #pragma nounroll
-            for (int e = l; e < 32 * CH; e += 64) {
-                const int n1 = e / CH, m = e % CH, q = m * B / 16, in = m * B % 16;
-                const char* from = piece + n1 * 128 + (q ^ (n1 >> 1 & 7)) * 16 + (BF ? in ^ (n1 >> 4) * 8 : in);
-                const int to = k * CH + m < mleft ? (j * 32 + n1) * (int)a.ldy * B + k * 128 + m * B : (int)0x80000000;
-                if constexpr (BF) __builtin_amdgcn_raw_buffer_store_b16(*(const uint16_t*)from, ybuf, to, 0, 0);
-                else __builtin_amdgcn_raw_buffer_store_b32(*(const uint32_t*)from, ybuf, to, 0, 0);
+            for (int n1 = rr; n1 < 32; n1 += 8) {
+                u32x4 o = *(const u32x4*)(piece + n1 * 128 + (c ^ (n1 >> 1 & 7)) * 16);
+                if (BF && n1 >= 16) o = u32x4{o[2], o[3], o[0], o[1]};
+                const int to = (j * 32 + n1) * (int)a.ldy * B + k * 128 + c * 16;
+                if (left >= 16 / B) {
+                    __builtin_amdgcn_raw_buffer_store_b128(o, ybuf, to, 0, 0);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < 16 / B; ++v)
+                        if (v < left) {
+                            if constexpr (BF) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(o[v / 2] >> (16 * (v & 1))), ybuf, to + v * B, 0, 0);
+                            else __builtin_amdgcn_raw_buffer_store_b32(o[v], ybuf, to + v * B, 0, 0);
+                        }
+                }
             }
         }
     };

@@ -4,7 +4,7 @@ import sys
 
 import pytest
 
-from test_gpu_experts8 import gen, swiglu64
+from test_gpu_experts8 import codes, dt, gen, product, same, scales, swiglu64
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +38,26 @@ def test_swiglu_rounds_its_quotient_once(sm, I):
     got, want = sm.swiglu(gu, out_dtype=torch.float32)[0].double(), swiglu64(gu)
     off = float(((got - want) / want).abs().max()) * 2.0 ** 24
     assert off <= 2.04, off
+
+
+# ---- the last channels of a tile ---------------------------------------------------------------
+
+@pytest.mark.parametrize("N,M,K", [(2100, 7168, 32), (300, 4096, 64), (300, 4096, 65)])   # tiles of 256, of 128, of odd rows
+@pytest.mark.parametrize("y", ["f32", "bf16"])
+def test_last_channels_of_a_tile(sm, N, M, K, y):
+    """Rows end at each place of a 16-byte piece, at the borders of 32, 64 and 128 channels, and on any
+    element of y; the columns behind stay."""
+    import torch
+    g = gen(N + K)
+    w, x = codes(g, M + 256, K), codes(g, N, K)
+    ws, xs = scales(g, M + 256), scales(g, N)
+    whole = product(x, xs, w, ws, y)
+    for tail in (1, 2, 3, 4, 5, 6, 7, 8, 9, 31, 33, 63, 65, 95, 100, 127, 129, 135, 191, 250, 255):
+        say("last channels", N, M + tail, K, y)
+        m = M + tail
+        for start in (0, 1):
+            yb = torch.full((start + N * (m + 3),), 7.0, device="cuda", dtype=dt(y))
+            out = yb[start:].view(N, m + 3)
+            sm.i8_gemv({"weight": w[:m], "scales": ws[:m]}, x, xs, m, K, y=out[:, :m])
+            same(out[:, :m], whole[:, :m])
+            assert bool((out[:, m:] == 7).all()) and bool((yb[:start] == 7).all())
