@@ -984,12 +984,15 @@ void launch(I8Args a, hipStream_t st) {
     const bool tiled = a.ldx <= 1 << 22 && a.ldy <= 1 << 20 && avg >= (a.offsets ? odd ? 33 : 9 : 49) &&
                        tiles64 >= (odd ? 256 : 128);
     if (!tiled) {
-        // as many rows a wave as an expert has, but enough waves' tiles (us by 64, 32, 16 rows: 61 x 5125 x 4150
-        // 13.0 15.4 29.7; 64 x 4096 x 4096 10.1 7.7; 300 x 500 x 5001 13.9 9.6 21; 64 x 1000 x 4096 9.7 6.8
-        // 7.8; 40 x 700 x 8192 13.7 9.7 8.6)
+        // As many rows a wave as an expert has, but 32 while their workgroups (8 waves share a tile) fit
+        // one a CU, and 16 where 32 give work to a quarter of the CUs.  us by 64, 32, 16 rows (rows x M x K):
+        // 33 x 4090 x 4096 (256 workgroups of 32 rows) 9.1 7.2 11.0, 33 x 4130 x 4096 (260) 9.2 10.8 14.7;
+        // 96 x 2720 x 4096 (255) 10.0 8.8 15.3, 96 x 2800 x 4096 (264) 9.1 9.1; 61 x 4500 x 4150 (282) 12.4
+        // 15.2 28.6; 4 experts of 800 x 4096 with 50 rows each 9.8 8.9, 2 of 1900 x 4096 with 60 10.1 10.6;
+        // 32 x 2048 x 4096 (64) 8.4 6.5 6.4, 40 x 700 x 8192 (44) 11.9 9.1 8.5.
         const int64_t tm32 = (a.M - 1) / 32 + 1;
         int jn = avg <= (a.offsets ? 8 : 16) ? 1 : avg <= 32 ? 2 : 4;
-        if (jn == 4 && row_tiles(a, 64) * tm32 < 144) jn = 2;
+        if (jn == 4 && row_tiles(a, 32) * tm32 <= 256) jn = 2;
         if (jn == 2 && row_tiles(a, 32) * tm32 < 64) jn = 1;
         odd ? launch_rows_jn<true>(a, jn, st) : launch_rows_jn<false>(a, jn, st);
     } else if (!odd && (a.offsets ? avg >= 176 : row_tiles(a, 256) * ((a.M - 1) / 256 + 1) >= 224)) {

@@ -105,3 +105,16 @@ def test_grids_that_hip_takes(driver):
     for t in took:
         assert t and all(0 < n <= 1 << 22 for _, n in t), t[:3]
     assert sum(n for _, n in took[1]) >= (1 << 30) // 64
+
+
+# calls on both sides of a rule, and the kernel that is faster there
+BORDERS = [
+    (gemv(33, 4090, 4096), "k_i8_rows<2, 2"), (gemv(33, 4130, 4096), "k_i8_rows<2, 4"),      # 256 and 260 workgroups
+    (gemv(96, 2720, 4096), "k_i8_rows<2, 2"), (gemv(61, 4500, 4150), "k_i8_rows<2, 4"),
+    (gemv(200, 800, 4096, E=4), "k_i8_rows<2, 2"), (gemv(120, 1900, 4096, E=2), "k_i8_rows<2, 4"),
+]
+
+
+def test_rules_at_their_borders(driver):
+    for (query, kernel), took in zip(BORDERS, ask(driver, [q for q, _ in BORDERS])[1]):
+        assert [k[:len(kernel)] for k, _ in took] == [kernel], (query, kernel, took)
