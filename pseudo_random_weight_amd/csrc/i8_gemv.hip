@@ -965,10 +965,22 @@ void launch_rows_jn(const I8Args& a, int jn, hipStream_t st) {
 //   with 16 rows each 126 (166), with 40 rows 174 (179), with 128 rows 330 (248).
 //   Tiles of 128 channels by 64 or 128 rows: by 128 where that makes most of a workgroup a CU.
 //   256 x 8192 x 2048: 10.1 by 64, 11.7 by 128; 512 x 8192 x 2048: 17.1 and 14.1.
-//   Tiles of 256 by 256, one a CU: where there is one for nearly each CU.  1024 x 8192 x 2048: 33
-//   (128 by 128: 25.8), 2048 x 8192 x 2048: 42.6 (51.5).  With experts by their rows: 100 experts of
+//   Tiles of 256 by 256, one a CU: where there is one for nearly each CU, and no second round for a
+//   few.  By number of tiles, 256 by 256 (128 by 128), K = 512: 192 16.5 (14.6), 224 17.0 (17.1), 256
+//   17.9 (17.9), 288 27.6 (20.9), 352 27.7 (24.5), 400 28.1 (27.6), 448 29.2 (29.5), 512 31.6 (33.0);
+//   K = 1024: 192 22.0 (21.2), 224 22.8 (24.7), 288 36.5 (30.3), 352 37.2 (36.8), 400 38.7 (40.4), 512 43.8
+//   (51.8); K = 2048: 192 32.1 (36.4), 256 36.3 (47.0), 264 53.4 (55.8), 288 56.3 (56.0), 512 70.4 (92.4); K =
+//   4096: 192 51.6 (64.3), 264 89.0 (98.8), 288 96.6 (103.5).  (K = 256: 14.5 for 15.3 at 256, 24.0 for 25.4
+//   at 512; a third round for a few is not looked for: K = 512, 576 tiles 42.1 (36.9), K = 1024 59.0 (59.2).)
+//   With experts by their rows, counted from N, for which dropped slots count too: 100 experts of
 //   2048 x 2048 with 164 rows each 152 (150), with 240 rows 176 (193), 328 rows 222 (244); 8 of
 //   8192 x 4096 with 128 rows 86 (80), with 192 rows 93 (104).
+bool wide_pays(const I8Args& a, int avg) {
+    if (a.offsets) return avg >= 176;
+    const int64_t tiles = row_tiles(a, kWideN) * ((a.M - 1) / kWideM + 1);
+    return tiles >= (a.K >= 1536 ? 192 : 224) && (tiles <= 256 || a.K >= 2048 || (tiles - 256) * a.K >= 90000);
+}
+
 void launch(I8Args a, hipStream_t st) {
     if (a.K < 16) {
         a.tm = (a.M - 1) / 64 + 1;
@@ -995,7 +1007,7 @@ void launch(I8Args a, hipStream_t st) {
         if (jn == 4 && row_tiles(a, 32) * tm32 <= 256) jn = 2;
         if (jn == 2 && row_tiles(a, 32) * tm32 < 64) jn = 1;
         odd ? launch_rows_jn<true>(a, jn, st) : launch_rows_jn<false>(a, jn, st);
-    } else if (!odd && (a.offsets ? avg >= 176 : row_tiles(a, 256) * ((a.M - 1) / 256 + 1) >= 224)) {
+    } else if (!odd && wide_pays(a, avg)) {
         launch_wide(a, st);
     } else if (row_tiles(a, 128) * tm < 192) {
         odd ? launch_odd<2, 1>(a, st) : launch_mid<2, 1>(a, st);

@@ -111,6 +111,9 @@ def test_grids_that_hip_takes(driver):
 BORDERS = [
     (gemv(33, 4090, 4096), "k_i8_rows<2, 2"), (gemv(33, 4130, 4096), "k_i8_rows<2, 4"),      # 256 and 260 workgroups
     (gemv(96, 2720, 4096), "k_i8_rows<2, 2"), (gemv(61, 4500, 4150), "k_i8_rows<2, 4"),
+    (gemv(1536, 8192, 1024), "k_i8_mid<2, 2"), (gemv(1536, 8192, 2048), "k_i8_wide"),        # 192 tiles
+    (gemv(1792, 8192, 1024), "k_i8_wide"), (gemv(2304, 8192, 512), "k_i8_mid<2, 2"),         # 224, 288
+    (gemv(2304, 8192, 4096), "k_i8_wide"), (gemv(3584, 8192, 512), "k_i8_wide"),             # 288, 448
     (gemv(200, 800, 4096, E=4), "k_i8_rows<2, 2"), (gemv(120, 1900, 4096, E=2), "k_i8_rows<2, 4"),
 ]
 

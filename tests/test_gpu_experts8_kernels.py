@@ -32,7 +32,9 @@ ONE = [
     ("k_i8_mid<2, 2", 1000, 3200, 80), ("k_i8_mid<2, 2", 1001, 3300, 156),
     ("k_i8_odd<2, 1", 300, 6600, 65), ("k_i8_odd<2, 1", 257, 6800, 130),
     ("k_i8_odd<2, 2", 1000, 3200, 71), ("k_i8_odd<2, 2", 1001, 3300, 257),
-    ("k_i8_wide", 3600, 4608, 1024), ("k_i8_wide", 3600, 4600, 1028),
+    ("k_i8_wide", 3500, 4608, 1024), ("k_i8_wide", 2000, 7200, 148), ("k_i8_wide", 1536, 8190, 1536),
+    # several tiles a workgroup, and a last round for some of the workgroups only
+    ("k_i8_wide", 5000, 7600, 272), ("k_i8_wide", 4100, 8190, 324), ("k_i8_wide", 9000, 5003, 1024),
 ]
 
 
