@@ -126,51 +126,42 @@ __device__ __forceinline__ void wave_order() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// 16 bytes from column k of a row, zeros past K.  Any alignment.
-__device__ __forceinline__ u32x4 load16(const int8_t* row, int k, int K) {
-    u32x4 v = {0, 0, 0, 0};
-    if (k + 16 <= K) {
-        __builtin_memcpy(&v, row + k, 16);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (k + i < K) v[i / 4] |= (uint32_t)(uint8_t)row[k + i] << (8 * (i & 3));
-    }
-    return v;
-}
-
 // Rows of fewer than 16 columns, which no 16-byte load fits: a tile of 64 channels by 64 rows, each of
-// four waves a quarter of it in 16 x 16 x 64 instructions, both operands through LDS.
+// four waves a quarter of it in 16 x 16 x 64 instructions.  A thread loads a row, a byte at a time and
+// zeros past K; the row is the first of the four pieces that an instruction takes, zeros the others.
+// Bound by the outputs' writes, in single elements: 4096 rows of 8192 channels, 8 columns, 70 us; one row
+// of 2^20 channels 31.
 __global__ __launch_bounds__(256) void k_i8_tile(const I8Args a) {
-    __shared__ u32x4 ws[64][5], xs[64][5];
+    __shared__ u32x4 ws[64], xs[64];
     const int64_t b = a.first + blockIdx.x;
     const Rows r = find_rows(a, b / a.tm, 64);
     if (r.n == 0) return;
     const int64_t m0 = b % a.tm * 64;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int c = lane & 15, q = lane >> 4, wm = wave & 1, wn = wave >> 1;
-    const int lr = tid >> 2, lc = tid & 3;
-    const int8_t* wrow = a.w + ((int64_t)r.e * a.M + (m0 + lr < a.M ? m0 + lr : a.M - 1)) * a.K;
-    const int8_t* xrow = a.x + (r.row0 + (int64_t)(lr < r.n ? lr : r.n - 1)) * a.ldx;
-    i32x4 acc[2][2] = {};
-    for (int k0 = 0; k0 < a.K; k0 += 64) {
-        const u32x4 wv = load16(wrow, k0 + 16 * lc, a.K), xv = load16(xrow, k0 + 16 * lc, a.K);
-        __syncthreads();
-        ws[lr][lc] = wv;
-        xs[lr][lc] = xv;
-        __syncthreads();
-        i32x4 wf[2], xf[2];
+    if (tid < 128) {
+        const int lr = tid & 63;
+        const int8_t* row = tid < 64 ? a.w + ((int64_t)r.e * a.M + (m0 + lr < a.M ? m0 + lr : a.M - 1)) * a.K
+                                     : a.x + (r.row0 + (int64_t)(lr < r.n ? lr : r.n - 1)) * a.ldx;
+        u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 15; ++i)
+            if (i < a.K) v[i / 4] |= (uint32_t)(uint8_t)row[i] << (8 * (i & 3));
+        (tid < 64 ? ws : xs)[lr] = v;
+    }
+    __syncthreads();
+    i32x4 wf[2] = {}, xf[2] = {}, acc[2][2] = {};
+    if (q == 0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            wf[i] = __builtin_bit_cast(i32x4, ws[wm * 32 + i * 16 + c][q]);
-            xf[i] = __builtin_bit_cast(i32x4, xs[wn * 32 + i * 16 + c][q]);
+            wf[i] = __builtin_bit_cast(i32x4, ws[wm * 32 + i * 16 + c]);
+            xf[i] = __builtin_bit_cast(i32x4, xs[wn * 32 + i * 16 + c]);
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[i], xf[j], acc[i][j], 0, 0, 0);
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[i], xf[j], acc[i][j], 0, 0, 0);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int n = wn * 32 + j * 16 + c;

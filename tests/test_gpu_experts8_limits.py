@@ -4,7 +4,7 @@ import sys
 
 import pytest
 
-from test_gpu_experts8 import codes, dt, gen, product, same, scales, swiglu64
+from test_gpu_experts8 import codes, dt, gen, product, same, scales, sizes_to_offsets, swiglu64
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +61,30 @@ def test_last_channels_of_a_tile(sm, N, M, K, y):
             sm.i8_gemv({"weight": w[:m], "scales": ws[:m]}, x, xs, m, K, y=out[:, :m])
             same(out[:, :m], whole[:, :m])
             assert bool((out[:, m:] == 7).all()) and bool((yb[:start] == 7).all())
+
+
+# ---- rows of fewer than 16 columns -------------------------------------------------------------
+
+@pytest.mark.parametrize("K", range(18))
+def test_rows_of_few_columns(sm, K):
+    """Every length below a 16-byte piece and the first above, rows on any byte, whole and partial
+    tiles, one matrix and many: codes behind a row's end belong to the next row and do not count."""
+    import torch
+    say("few columns", K)
+    g = gen(K)
+    for N, M in ((1, 1), (1, 70), (64, 64), (130, 200), (65, 63)):
+        for ldx, offset in ((K, 0), (K + 5, 3)):
+            x = codes(g, N * ldx + 16)[offset:offset + N * ldx].view(N, ldx)[:, :K]
+            w = codes(g, M * K + 16)[offset:offset + M * K].view(M, K)
+            xs, ws = scales(g, N), scales(g, M)
+            same(sm.i8_gemv({"weight": w, "scales": ws}, x, xs, M, K), product(x, xs, w, ws, "f32"))
+    counts = [0, 3, 0, 130, 1] * 60
+    E, M, N = len(counts), 66, sum(counts) + 4
+    w, x, ws, xs = codes(g, E, M, K), codes(g, N, K), scales(g, E, M), scales(g, N)
+    out = torch.full((N, M), 3.0, device="cuda")
+    sm.i8_gemv({"weight": w, "scales": ws}, x, xs, M, K, y=out, offsets=sizes_to_offsets(counts))
+    e = torch.repeat_interleave(torch.arange(E, device="cuda"), torch.tensor(counts, device="cuda"))
+    live = N - 4
+    d = (w[e].double() * x[:live, None].double()).sum(dim=2)
+    same(out[:live], d.float() * xs[:live, None] * ws[e])
+    assert bool((out[live:] == 3).all())
