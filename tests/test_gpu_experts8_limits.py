@@ -1,5 +1,6 @@
 """GPU tests of the operators of 8-bit experts at the borders of what their documentation
 promises: rounding, what is read and written, many experts, and replays with other routings."""
+import math
 import sys
 
 import pytest
@@ -88,3 +89,45 @@ def test_rows_of_few_columns(sm, K):
     d = (w[e].double() * x[:live, None].double()).sum(dim=2)
     same(out[:live], d.float() * xs[:live, None] * ws[e])
     assert bool((out[live:] == 3).all())
+
+
+# ---- offsets of any values ---------------------------------------------------------------------
+
+WRONG = [lambda N: [0, N // 10, 2 ** 31 - 1, N // 20, N // 2, N], lambda N: [-2 ** 31, 2 * N // 5, N // 5, N, N, 3],
+         lambda N: [N - 1, N + 1, 3 * N, N // 2, 0, N], lambda N: [0, N, 0, N, 0, N], lambda N: [-5, -4, -3, -2, -1, -1],
+         lambda N: [-9, N // 3, N // 3, N + 7, 2 * N, 2 ** 31 - 1], lambda N: [N // 4, N // 4 + 1, N // 2, N // 2, N - 2, N - 1],
+         lambda N: [N, N // 2, N // 3, N // 4, N // 5, 0]]
+
+
+@pytest.mark.parametrize("N,K", [(20, 144), (100, 128), (400, 144), (400, 145), (1500, 144), (9000, 148), (9000, 163), (300, 15)])
+@pytest.mark.parametrize("case", range(len(WRONG)))
+def test_wrong_offsets_give_wrong_rows_only(sm, N, K, case):
+    """Values are taken as the nearer end of [0, N].  Runs that do not overlap are exact; a row that
+    several experts claim holds values of theirs or its old ones; a row of none stays.  Around x, its
+    scales, the weights and y lie other codes, NaN and marks: a row read beside them would show."""
+    import torch
+    say("wrong offsets", N, K, case)
+    g = gen(N + K)
+    M, E, pad = 640, 5, 300
+    x = codes(g, N + 2 * pad, K)[pad:pad + N]
+    xsb = torch.full((N + 2 * pad,), math.nan, device="cuda")
+    xs = xsb[pad:pad + N]
+    xs.copy_(scales(g, N))
+    w, ws = codes(g, E + 2, M, K)[1:-1], scales(g, E, M)
+    off = WRONG[case](N)
+    yb = torch.full((N + 2 * pad, M), 5.0, device="cuda")
+    sm.i8_gemv({"weight": w, "scales": ws}, x, xs, M, K, y=yb[pad:pad + N],
+               offsets=torch.tensor(off, dtype=torch.int32, device="cuda"))
+    ends = [min(max(v, 0), N) for v in off]
+    runs = [(e, a, b) for e, (a, b) in enumerate(zip(ends, ends[1:])) if a < b]
+    claims = torch.zeros(N, dtype=torch.int32, device="cuda")
+    for _, a, b in runs:
+        claims[a:b] += 1
+    y = yb[pad:pad + N]
+    fits = (y == 5) & (claims != 1)[:, None]
+    for e, a, b in runs:
+        fits[a:b] |= y[a:b] == product(x[a:b], xs[a:b], w[e], ws[e], "f32")
+    if sum(b - a for _, a, b in runs) > N:         # more tiles than there can be: some of them may be left out
+        fits |= y == 5
+    assert bool(fits.all())
+    assert bool((yb[:pad] == 5).all()) and bool((yb[pad + N:] == 5).all())
