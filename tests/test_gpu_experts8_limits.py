@@ -3,9 +3,11 @@ promises: rounding, what is read and written, many experts, and replays with oth
 import math
 import sys
 
+import numpy as np
 import pytest
 
-from test_gpu_experts8 import codes, dt, gen, product, same, scales, sizes_to_offsets, swiglu64
+from test_gpu_experts8 import codes, dt, gen, layer_inputs, order, product, routing, same, scales, sizes_to_offsets, \
+    swiglu64
 
 pytestmark = pytest.mark.gpu
 
@@ -131,3 +133,76 @@ def test_wrong_offsets_give_wrong_rows_only(sm, N, K, case):
         fits |= y == 5
     assert bool(fits.all())
     assert bool((yb[:pad] == 5).all()) and bool((yb[pad + N:] == 5).all())
+
+
+# ---- captured calls with another routing at each replay ------------------------------------------
+
+@pytest.mark.parametrize("T,k,E,H,I", [(3, 4, 9, 200, 72),          # sorted in one launch
+                                       (70, 4, 9, 200, 72), (900, 4, 9, 204, 72),       # by chunks, summed directly
+                                       (2500, 8, 600, 48, 32),      # by chunks, summed once for all
+                                       (1600, 2, 5, 160, 96)])      # tiles of 256 rows
+def test_replays_with_other_routings(sm, T, k, E, H, I):
+    """The order, the offsets, the number of rows that exist and the tiles' experts are new at each
+    replay: random ones, all slots dropped, all tokens at one expert, none dropped.  Outputs and scratch
+    hold other values before it."""
+    import torch
+    say("replays", T, k, E, H, I)
+    ids, w, x, xs, gu, dn = layer_inputs(T, k, E, H, I, 0.2, T)
+    bf, f32, i8, i32 = torch.bfloat16, torch.float32, torch.int8, torch.int32
+    shapes = {"rows": ((T * k, H), i8), "scale": ((T * k,), f32), "off": ((E + 1,), i32), "inv": ((T, k), i32),
+              "a": ((T * k, 2 * I), bf), "h": ((T * k, I), i8), "hs": ((T * k,), f32), "d": ((T * k, H), f32),
+              "y": ((T, H), f32), "dr": ((T * k, H), f32), "dw": ((T, k), f32), "layer": ((T, H), f32)}
+    n_ws = sm.moe_sort_workspace_bytes(T, k, E)
+
+    def buffers():
+        b = {n: torch.empty(s, dtype=t, device="cuda") for n, (s, t) in shapes.items()}
+        b["sort_ws"] = torch.empty(n_ws, dtype=torch.uint8, device="cuda") if n_ws else None
+        b["layer_ws"] = torch.empty(sm.moe_i8_workspace_bytes(T, k, E, H, I), dtype=torch.uint8, device="cuda")
+        return b
+
+    def poison(b, v):
+        for t in b.values():
+            if t is not None:
+                t.fill_(v)
+
+    def run(b):
+        sm.moe_sort(x, ids, E, x_scale=xs, rows=b["rows"], row_scale=b["scale"], offsets=b["off"], inverse=b["inv"],
+                    workspace=b["sort_ws"])
+        sm.i8_gemv(gu, b["rows"], b["scale"], 2 * I, H, y=b["a"], offsets=b["off"])
+        sm.swiglu(b["a"], out=b["h"], scale=b["hs"], count=b["off"][E:])
+        sm.i8_gemv(dn, b["h"], b["hs"], H, I, y=b["d"], offsets=b["off"])
+        sm.moe_unsort(b["d"], b["inv"], w, y=b["y"])
+        sm.moe_unsort_grad(b["y"], b["d"], b["inv"], w, drows=b["dr"], dw=b["dw"])
+        sm.moe_i8(ids, w, x, xs, E, H, I, gu, dn, y=b["layer"], workspace=b["layer_ws"])
+
+    got, want = buffers(), buffers()
+    st, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    run(got)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        run(got)
+        st.synchronize()
+        with torch.cuda.graph(graph, stream=st):
+            run(got)
+    one = torch.full((T, k), E // 2, dtype=i32, device="cuda")
+    for i, new in enumerate([routing(1, T, k, E, 0.5), torch.full_like(ids, -1), one, routing(2, T, k, E, 0.0),
+                             torch.where(one > 0, torch.full_like(one, E + 3), one), routing(3, T, k, E, 0.9), one.clone()]):
+        ids.copy_(new)
+        poison(got, 77)
+        poison(want, 99)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        run(want)
+        inv, off = order(new, E)
+        assert np.array_equal(got["off"].cpu().numpy(), off) and np.array_equal(got["inv"].cpu().numpy(), inv), i
+        live = int(off[-1])
+        for n in ("off", "inv", "y", "dw", "layer"):
+            same(got[n], want[n])
+        for n in ("rows", "scale", "a", "h", "hs", "d", "dr"):
+            same(got[n][:live], want[n][:live])
+            assert bool((got[n][live:] == 77).all()) and bool((want[n][live:] == 99).all()), (i, n)
+        gone = torch.from_numpy((inv < 0).all(axis=1)).cuda()
+        assert bool((got["layer"][gone] == 0).all())
+        if live:
+            same(got["rows"][torch.from_numpy(inv[inv >= 0]).cuda()], x.repeat_interleave(k, dim=0)[torch.from_numpy((inv >= 0).ravel()).cuda()])
