@@ -539,6 +539,9 @@ int seedmm_moe_block(const seedmm_block *block, void *r, int r_dtype, const void
  *   N: rows offsets[e] .. offsets[e + 1] - 1 belong to expert e (seedmm_moe_sort writes them).
  *   Rows of y from offsets[E] on are left as they were.  Values outside of [0, N] are taken as
  *   the nearer end, so a wrong array gives wrong rows, never an access outside of x and y.
+ *   Of rows that do not start on 4 bytes the aligned words of 4 bytes are read that hold them: up
+ *   to 3 bytes in front of and behind weight and x, in words with bytes of theirs.  No result
+ *   depends on these bytes.
  *   x: int8 [N][ldx];  x_scale: fp32[N];  y: [N][ldy] of y_dtype (SEEDMM_F32, SEEDMM_BF16),
  *   overwritten; columns M .. ldy - 1 are left as they were.
  *   The sums are exact (int32; all 256 codes); one is converted to fp32, multiplied by the row's

@@ -204,7 +204,9 @@ constexpr int kRowsWaves = 8;
 
 // 16 bytes at any address.  Loads that do not start on 4 bytes take the memory path several times
 // as long (61 x 5125 x 4150: 28.9 us where rows of 4160 took 11.5), so where rows may start anywhere
-// (ODD) the aligned words that hold the 16 bytes are loaded and shifted; no other words are.
+// (ODD) the aligned words that hold the 16 bytes are loaded and shifted; no other words are.  Up to 3
+// bytes in front of and behind a tensor share a word with its own, are loaded and shifted out: a word lies
+// in one page and one cache line, so these loads touch nothing that the tensor's do not.
 template <bool ODD>
 struct Bytes16 {
     u32x4 v;

@@ -135,6 +135,30 @@ def test_wrong_offsets_give_wrong_rows_only(sm, N, K, case):
     assert bool((yb[:pad] == 5).all()) and bool((yb[pad + N:] == 5).all())
 
 
+# ---- bytes beside the tensors --------------------------------------------------------------------
+
+@pytest.mark.parametrize("N,M,K", [(1, 100, 2049), (1, 33, 16), (16, 64, 258), (40, 130, 511), (300, 6600, 65), (1000, 3200, 71)])
+@pytest.mark.parametrize("offset", [1, 2, 3])
+def test_bytes_beside_the_rows_do_not_count(sm, N, M, K, offset):
+    """Weights and x on any byte, x as a whole and with rows apart: whatever stands in front of them,
+    behind them and between the rows, the bits are the same."""
+    import torch
+    say("bytes beside", N, M, K, offset)
+    g = gen(N + K + offset)
+    for ldx in (K, K + 3):
+        x, w, xs, ws = codes(g, N, K), codes(g, M, K), scales(g, N), scales(g, M)
+        want = product(x, xs, w, ws, "f32")
+        for beside in (0, 127, -128, None):
+            xb, wb = codes(g, N * ldx + 8), codes(g, M * K + 8)
+            if beside is not None:
+                xb.fill_(beside)
+                wb.fill_(beside)
+            xv, wv = xb[offset:offset + N * ldx].view(N, ldx)[:, :K], wb[4 - offset:4 - offset + M * K].view(M, K)
+            xv.copy_(x)
+            wv.copy_(w)
+            same(sm.i8_gemv({"weight": wv, "scales": ws}, xv, xs, M, K), want)
+
+
 # ---- captured calls with another routing at each replay ------------------------------------------
 
 @pytest.mark.parametrize("T,k,E,H,I", [(3, 4, 9, 200, 72),          # sorted in one launch
