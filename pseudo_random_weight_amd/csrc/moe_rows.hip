@@ -692,7 +692,10 @@ int seedmm_swiglu(const void* gate_up, int g_dtype, int64_t ldg, void* out, int 
 }
 
 // Scratch of one layer call: the order, the sorted rows, gate and up (whose room the down
-// product's rows take later), and the SwiGLU rows.
+// product's rows take later), and the SwiGLU rows.  Gate and up and the down product's rows are bf16: of
+// the layer's error against 64 bits, 2.041% of y, 2.034 remain with fp32 rows behind the down product,
+// nearly all of it from the 8-bit rows of the SwiGLU; they would take 495 us for 439 at 4096 tokens (8 of
+// 100 experts of 2048 x 1024).
 struct LayerPlan {
     size_t offsets, inverse, rows, row_scale, gu, h, h_scale, total;
 };

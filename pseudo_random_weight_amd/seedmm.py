@@ -964,7 +964,8 @@ def moe_i8(topk_ids, topk_w, x, x_scale, E, H, I, gate_up, down, y=None, workspa
     """y fp32 [T][H]: the routed SwiGLU layer of experts in 8-bit integers (seedmm_moe_i8).  x
     int8 [T][H] with x_scale fp32 [T] (add_norm's); gate_up, down: matrices as for i8_gemv, E
     stacked [2I][H] (gate rows, then up rows) and [H][I]; topk_ids int32 and topk_w fp32
-    [T][top_k], an id outside of [0, E) drops its slot."""
+    [T][top_k], an id outside of [0, E) drops its slot.  The rows behind both products are bf16; for
+    fp32 ones behind the second, call moe_sort, i8_gemv, swiglu, i8_gemv and moe_unsort."""
     if y is None:
         with _on(stream):
             y = torch.empty(_gpu(x, "x").shape, dtype=torch.float32, device=x.device)

@@ -230,3 +230,21 @@ def test_replays_with_other_routings(sm, T, k, E, H, I):
         assert bool((got["layer"][gone] == 0).all())
         if live:
             same(got["rows"][torch.from_numpy(inv[inv >= 0]).cuda()], x.repeat_interleave(k, dim=0)[torch.from_numpy((inv >= 0).ravel()).cuda()])
+
+
+# ---- the layer's bf16 rows -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("T,k,E,H,I", [(1, 8, 100, 512, 256), (64, 8, 100, 512, 256), (900, 4, 9, 200, 72)])
+def test_layer_rows_cost_half_a_step_of_bf16(sm, T, k, E, H, I):
+    """The five calls with fp32 rows behind the down product: the layer differs from them by half a
+    step of bf16 (2^-8) of each slot's row at most, and both sums' k half steps of fp32."""
+    import torch
+    say("layer's rows", T, k, E, H, I)
+    ids, w, x, xs, gu, dn = layer_inputs(T, k, E, H, I, 0.1, T)
+    rows, rs, off, inv = sm.moe_sort(x, ids, E, x_scale=xs)
+    a = sm.i8_gemv(gu, rows, rs, 2 * I, H, y_dtype=torch.bfloat16, offsets=off)
+    h, hs = sm.swiglu(a, out_dtype=torch.int8, count=off[E:])
+    d = sm.i8_gemv(dn, h, hs, H, I, y_dtype=torch.float32, offsets=off)
+    sizes = sm.moe_unsort(d.abs(), inv, w).double()             # w >= 0
+    y, y32 = sm.moe_i8(ids, w, x, xs, E, H, I, gu, dn), sm.moe_unsort(d, inv, w)
+    assert bool(((y.double() - y32.double()).abs() <= sizes * (2.0 ** -8 + 3 * k * 2.0 ** -24)).all())
