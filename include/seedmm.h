@@ -529,7 +529,8 @@ int seedmm_moe_block(const seedmm_block *block, void *r, int r_dtype, const void
  * Rows of any leading dimension and alignment (of their type) are taken; rows that start on 16
  * bytes are faster.  No result depends on the order in which anything runs: the same call
  * gives the same bits, and a token's result does not depend on the batch around it.  Outputs
- * overlap neither inputs nor each other, but where a call says so.
+ * overlap neither inputs nor each other, but where a call says so.  Gradients are there for the
+ * moves of rows (sort, unsort); the products, the SwiGLU step and the layer have none.
  *
  * seedmm_i8_gemv -- Y[n] = W X[n] for N rows of 8-bit integers with a scale a row, W in 8-bit
  * integers with a scale a channel, for one matrix or one an expert:

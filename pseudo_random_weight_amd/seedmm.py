@@ -5,6 +5,11 @@ plus sizes, on torch's current HIP stream or the one passed in (outputs and scra
 binding allocates belong to that stream).  Every step of the computation runs in
 the library's kernels; there is no Python or CPU fallback, and a missing library
 raises at import.
+
+No call records a gradient: a result carries no graph, whatever its inputs require.
+Where gradients are offered they are calls of their own (moe_unsort for moe_sort's
+rows, moe_unsort_grad for moe_unsort), for a torch.autograd.Function of the caller's;
+the products, swiglu and the layers have none.
 """
 from __future__ import annotations
 
@@ -919,7 +924,8 @@ def moe_unsort(rows: torch.Tensor, inverse: torch.Tensor, topk_w=None, y=None,
 
 def moe_unsort_grad(dy: torch.Tensor, rows: torch.Tensor, inverse: torch.Tensor,
                     topk_w: torch.Tensor, drows=None, dw=None, stream=None):
-    """(drows, dw): moe_unsort's gradients for dy fp32 or bf16 [T][H] (seedmm_moe_unsort_grad).
+    """(drows, dw): moe_unsort's gradients for dy fp32 or bf16 [T][H] (seedmm_moe_unsort_grad), to be
+    called by the caller's backward pass: moe_unsort itself records none.
     drows has rows' shape and type (rows that no slot names are left as they were; a drows
     allocated here holds no values there), dw is fp32 [T][top_k]."""
     if drows is None or dw is None:

@@ -248,3 +248,39 @@ def test_layer_rows_cost_half_a_step_of_bf16(sm, T, k, E, H, I):
     sizes = sm.moe_unsort(d.abs(), inv, w).double()             # w >= 0
     y, y32 = sm.moe_i8(ids, w, x, xs, E, H, I, gu, dn), sm.moe_unsort(d, inv, w)
     assert bool(((y.double() - y32.double()).abs() <= sizes * (2.0 ** -8 + 3 * k * 2.0 ** -24)).all())
+
+
+# ---- gradients -----------------------------------------------------------------------------------
+
+def test_gradients_through_a_function_of_the_callers(sm):
+    """The calls record no graph; a torch.autograd.Function made of them has the plain form's gradients.
+    Whole numbers, so that both are exact."""
+    import torch
+    T, k, E, H = 40, 3, 7, 96
+    g = gen(5)
+    ids = routing(5, T, k, E, 0.3)
+
+    class Mix(torch.autograd.Function):          # sort, then back with weights
+        @staticmethod
+        def forward(ctx, x, w):
+            rows, _, _, inv = sm.moe_sort(x, ids, E)
+            ctx.save_for_backward(rows, inv, w)
+            return sm.moe_unsort(rows, inv, w)
+
+        @staticmethod
+        def backward(ctx, dy):
+            rows, inv, w = ctx.saved_tensors
+            drows, dw = sm.moe_unsort_grad(dy.contiguous(), rows, inv, w)
+            return sm.moe_unsort(drows, inv), dw
+
+    x = torch.randint(-9, 10, (T, H), generator=g, device="cuda").float().requires_grad_()
+    w = torch.randint(-4, 5, (T, k), generator=g, device="cuda").float().requires_grad_()
+    dy = torch.randint(-9, 10, (T, H), generator=g, device="cuda").float()
+    live = ((ids >= 0) & (ids < E)).float()
+    want = torch.autograd.grad((x * (w * live).sum(dim=1, keepdim=True) * dy).sum(), (x, w))
+    got = torch.autograd.grad((Mix.apply(x, w) * dy).sum(), (x, w))
+    same(got[0], want[0])
+    same(got[1], want[1])
+    rows, _, _, inv = sm.moe_sort(x, ids, E)
+    assert not rows.requires_grad and not sm.moe_unsort(rows, inv, w).requires_grad
+    assert not sm.swiglu(x)[0].requires_grad
