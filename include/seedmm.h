@@ -621,6 +621,8 @@ int seedmm_moe_unsort_grad(const void *dy, int dy_dtype, int64_t ldd, const void
  *     h[n][i] = g / (1 + exp(-g)) * u,  g = gate_up[n][i],  u = gate_up[n][I + i]
  *   gate_up: [N][ldg] of g_dtype (SEEDMM_F32 or SEEDMM_BF16), ldg >= 2 I;
  *   out: [N][ldo] of out_dtype.  SEEDMM_F32, SEEDMM_BF16: h, computed in fp32, rounded once.
+ *   (Below g = -87 exp(g) is no normal fp32 number: h is off by up to 2^-149 (4 + |g|)(1 + |u|) more,
+ *   which a u of 1e30 makes visible; g = -infinity gives NaN, as the formula does.)
  *   SEEDMM_I8: codes round(h / scale[n]) in [-127, 127] with scale[n] = max_i |h| / 127 (at
  *   least 2^-126); a row that holds an infinity or NaN gets scale NaN and codes 0 (as
  *   seedmm_add_norm's).  scale: fp32[N] with SEEDMM_I8, NULL otherwise.

@@ -43,6 +43,24 @@ def test_swiglu_rounds_its_quotient_once(sm, I):
     assert off <= 2.04, off
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("u", [1.0, -1e20, 1e30, 3e38])
+def test_swiglu_of_gates_whose_exp_is_not_normal(sm, u, out):
+    """exp(g) below 2^-126 is off by 2^-149 at most; so are its product with g and g's with the
+    quotient, before they meet u.  The rest as in test_swiglu: 8 half steps, the output's, and half
+    of the output's smallest number."""
+    import torch
+    g = torch.linspace(-112, -80, 4001, device="cuda")
+    gu = torch.stack([g, torch.full_like(g, u)]).t().contiguous()
+    got, want = sm.swiglu(gu, out_dtype=dt(out))[0][:, 0].double(), swiglu64(gu)[:, 0]
+    half = 8 * 2.0 ** -24 + (2.0 ** -8 if out == "bf16" else 0.0)
+    tiny = 2.0 ** -149 * (4 + g.double().abs()) * (1 + abs(u)) + (2.0 ** -134 if out == "bf16" else 0.0)
+    assert bool(((got - want).abs() <= 1.01 * half * want.abs() + tiny).all())
+    inf = torch.tensor([[-math.inf, u], [math.nan, u], [1.0, math.inf]], device="cuda")
+    got = sm.swiglu(inf, out_dtype=dt(out))[0][:, 0]
+    assert bool(got[:2].isnan().all()) and float(got[2]) == math.inf
+
+
 # ---- the last channels of a tile ---------------------------------------------------------------
 
 @pytest.mark.parametrize("N,M,K", [(2100, 7168, 32), (300, 4096, 64), (300, 4096, 65)])   # tiles of 256, of 128, of odd rows
