@@ -711,9 +711,9 @@ __global__ __launch_bounds__(256, 2) void k_i8_odd(const I8Args a) {
 // many tiles whatever the routing; and a tile of up to 128 rows, the rest of most experts, has half
 // of the products.  4096 tokens to 8 of 100 experts of 2048 x 2048: 214 us, 227 without both.
 //
-// 4096 x 8192 x 2048 (M x K, rows): 70 us, 8192 x 8192 x 8192: 435 us or 2530 TOP/s at 1.6 GHz, the clock
-// that the card's power leaves (1.9 GHz without the loads, 2.3 with a quarter of the products); 73%
-// of the cycles feed the matrix unit.  A tile's results take 7.8 us of 36 at K = 2048: all CUs write
+// 4096 x 8192 x 2048 (rows, M, K): 70 us, 8192 x 8192 x 8192: 437 us or 2516 TOP/s at 1.6 GHz, the clock
+// that the card's power leaves (1.9 GHz without the loads, 2.3 with a quarter of the products; another
+// card reached 412, 2670 TOP/s); 73% of the cycles feed the matrix unit.  A tile's results take 7.8 us of 36 at K = 2048: all CUs write
 // at 4.3 TB/s then.  Not waiting for the stores in the next tile's first step gained nothing.
 // ----------------------------------------------------------------------------------
 constexpr int kWideStep = 128, kWideM = 256, kWideN = 256;
@@ -948,7 +948,7 @@ void launch_rows_jn(const I8Args& a, int jn, hipStream_t st) {
     else launch_rows_kw<2, 4, 128, ODD>(a, st);
 }
 
-// Which kernel (us, each on the other's side too; M x K, rows):
+// Which kernel (us, each on the other's side too; M x K and rows, or rows x M x K):
 //   fewer than 16 columns: k_i8_tile.
 //   Few rows (an expert has on average), or a grid of few tiles: k_i8_rows reads the weights once
 //   and splits K over a workgroup's waves.  8192 x 2048: 49 rows 8.3 (tiles of 64: 9.2), 64 rows 8.2

@@ -27,8 +27,10 @@ __device__ __forceinline__ uint32_t wave_usum(uint32_t v) {
 //   DIRECT: larger ones are cut into chunks, whose experts k_sort_count counts; each workgroup
 //     sums the chunks' counts itself and counts ids inside its own chunk only.
 //   SCANNED: where those sums are long, k_sort_scan and k_sort_base make them once for all.
-// Bound by the rows' copies: 4096 tokens of 8 slots over 100 experts, 2048 columns of 8 bits: 36 us,
-// 3.8 TB/s; 5 of them are k_sort_count and the launch between.  One token: 2.8 us, a launch.
+// Long rows are bound by their copies: 4096 tokens of 8 slots over 100 experts, 2048 columns, bf16: 36 us,
+// 3.9 TB/s, 8 bits: 20 us, 3.5 TB/s; 5 of each are k_sort_count and the launch between.  Short ones by the
+// places: every token's workgroup reads its chunk's ids, so 16384 tokens of 16 slots over 512 experts take
+// 47 us with 64 bf16 columns, whose bytes need 6.  One token: 2.8 us, a launch.
 // ----------------------------------------------------------------------------------
 constexpr int kSortOnce = 1024;      // pairs
 constexpr int kSortChunk = 1024;     // pairs of a chunk, rounded down to whole tokens
@@ -258,7 +260,7 @@ __global__ __launch_bounds__(256) void k_sort(const SortArgs a, int64_t first) {
 // slot loads the token's places and weights, and they are handed out by lane reads (loaded by every
 // lane for each slot and pass they cost 4096 tokens of 8 slots 39 us for 32.5); the rows of 8
 // slots are in flight at once.  Bound by memory: 4096 tokens of 8 slots, 2048 columns, bf16 to fp32
-// in 32 us (4.9 TB/s), their gradients in 58 (4.7), 1021 tokens of 6 slots and 7167 columns in fp32
+// in 32 us (4.8 TB/s), their gradients in 58 to 61 (4.7), 1021 tokens of 6 slots and 7167 columns in fp32
 // in 86 (4.3; rows start on 4 bytes); 64 tokens of 8 slots 2.9 and 4.4 us.
 // ----------------------------------------------------------------------------------
 struct UnsortArgs {
@@ -388,7 +390,8 @@ __global__ __launch_bounds__(256) void k_unsort_grad(const UnsortArgs a) {
 // seedmm_swiglu.  TPR threads a row, NP pieces of 8 columns a thread held in registers; for 8
 // bits the row's largest |h| is found before the codes are written.  To floats bound by memory: 29491
 // of 32768 rows of 1024, bf16 to bf16, in 37 us (4.9 TB/s; 41 with a division).  To 8 bits by the arithmetic:
-// 43 us (3.5 TB/s; 55 with divisions).  512 rows to 8 bits 3.4 us, a launch.
+// 43 to 46 us (3.3 to 3.5 TB/s; 55 with divisions), the vector units busy for 79% of the cycles.  512 rows to
+// 8 bits 3.4 us, a launch.
 // ----------------------------------------------------------------------------------
 struct SwigluArgs {
     const void* gu;           // [N][ldg]
