@@ -202,6 +202,11 @@ class SideStream:
     def __init__(self, device=None):
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         self.stream = torch.cuda.Stream(device=dev)          # default priority
+        # torch deals its streams out of a pool of 32 in turn, so a program's own stream (that of a
+        # capture, say) may be this very one; then the calls take another of the pool
+        self.spare = torch.cuda.Stream(device=dev)
+        while self.spare.cuda_stream == self.stream.cuda_stream:
+            self.spare = torch.cuda.Stream(device=dev)
         self.fork = torch.cuda.Event()
         self.join = torch.cuda.Event()
         # torch creates an event on its first record: record both once so handles exist
@@ -209,8 +214,10 @@ class SideStream:
         self.join.record(self.stream)
         self.stream.synchronize()
 
-    def c(self) -> SeedSide:
-        return SeedSide(self.stream.cuda_stream, self.fork.cuda_event, self.join.cuda_event)
+    def c(self, main: int = 0) -> SeedSide:
+        """For a call on the stream with handle `main`, which the second stream is not."""
+        second = self.stream.cuda_stream
+        return SeedSide(second if second != main else self.spare.cuda_stream, self.fork.cuda_event, self.join.cuda_event)
 
 
 def _check(status: int, what: str):
@@ -416,7 +423,7 @@ def moe(topk_ids, topk_w, x, E, H, I, P, gate, up, down, y=None, workspace=None,
         arr = (ctypes.c_void_p * 5)(*[getattr(ev, "cuda_event", ev) for ev in events])
         _check(_lib.seedmm_moe_timed(*args, arr), "seedmm_moe_timed")
     elif side is not None:
-        sd = side.c()
+        sd = side.c(args[-1].value or 0)
         _check(_lib.seedmm_moe_ex(*args[:10], None, *args[10:], ctypes.byref(sd)),
                "seedmm_moe_ex")
     else:
@@ -466,7 +473,7 @@ def moe_mixed(topk_ids, topk_w, x, E, H, I, p4mask, gate, up, down, y=None, work
     rest = (_seedmat(gate), _seedmat(up), _seedmat(down), _ptr(workspace),
             workspace.numel() * workspace.element_size(), _stream(stream))
     if side is not None:
-        sd = side.c()
+        sd = side.c(rest[-1].value or 0)
         _check(_lib.seedmm_moe_ex(*args, 0, _ptr(p4mask), *rest, ctypes.byref(sd)),
                "seedmm_moe_ex")
     else:
@@ -841,14 +848,16 @@ class MoeBlock:
             raise TypeError("the workspace must be a tensor")
         if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("the workspace must be a contiguous tensor on the layer's device")
-        sd = None if side is None else ctypes.byref(side.c())
         ptr = lambda t: None if t is None else t.data_ptr()
         handle = _handle(stream, r)
+        if handle is None:
+            handle = _current_stream_handle(dev)
+        sd = None if side is None else ctypes.byref(side.c(handle))
         with torch.cuda.device(dev):
             _check(_lib.seedmm_moe_block(
                 ctypes.byref(self._c), r.data_ptr(), rd, ptr(delta), dd, y.data_ptr(), ptr(ids),
                 ptr(w), T, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                _current_stream_handle(dev) if handle is None else handle, sd), "seedmm_moe_block")
+                handle, sd), "seedmm_moe_block")
         return y
 
 
