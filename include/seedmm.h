@@ -642,8 +642,8 @@ int seedmm_swiglu(const void *gate_up, int g_dtype, int64_t ldg, void *out, int 
  *   by seedmm_moe_sort, seedmm_i8_gemv (gate and up at once, bf16 rows), seedmm_swiglu (8-bit
  *   rows), seedmm_i8_gemv (bf16 rows) and seedmm_moe_unsort, with their results: an id outside
  *   of [0, E) drops its slot, a token without slots gets 0.  The rows between are bf16, each
- *   value off by 2^-8 of itself at most, sums are fp32.  Gate and up are rounded to 8 bits next, by
- *   up to 1/254 of a row's largest; the down product's rows carry that error, some 2% of their
+ *   value off by 2^-8 of itself at most, sums are fp32.  What gate and up give is rounded to 8 bits
+ *   next, by up to 1/254 of a row's largest; the down product's rows carry that error, some 2% of their
  *   length, and bf16 adds 0.1 to 0.2% to it: against 64 bits the layer is off by 2.041% of y, by
  *   2.034% with fp32 rows behind the down product (64 tokens, 8 of 100 experts of 2048 x 1024),
  *   which take 495 us for 439 at 4096 tokens.  A caller who wants them makes the five calls, with

@@ -713,8 +713,9 @@ __global__ __launch_bounds__(256, 2) void k_i8_odd(const I8Args a) {
 //
 // 4096 x 8192 x 2048 (rows, M, K): 70 us, 8192 x 8192 x 8192: 437 us or 2516 TOP/s at 1.6 GHz, the clock
 // that the card's power leaves (1.9 GHz without the loads, 2.3 with a quarter of the products; another
-// card reached 412, 2670 TOP/s); 73% of the cycles feed the matrix unit.  A tile's results take 7.8 us of 36 at K = 2048: all CUs write
-// at 4.3 TB/s then.  Not waiting for the stores in the next tile's first step gained nothing.
+// card reached 412, 2670 TOP/s); 73% of the cycles feed the matrix unit.  A tile's results take 7.8 us of
+// 36 at K = 2048: all CUs write at 4.3 TB/s then.  Not waiting for the stores in the next tile's first
+// step gained nothing.
 // ----------------------------------------------------------------------------------
 constexpr int kWideStep = 128, kWideM = 256, kWideN = 256;
 
